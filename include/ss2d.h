@@ -55,7 +55,11 @@ typedef enum {
 } ss2d_status;
 
 /* Element type codes of the tensors that accept more than one type. */
-typedef enum { SS2D_F32 = 0, SS2D_BF16 = 1 } ss2d_dtype;
+typedef enum {
+    SS2D_F32 = 0,
+    SS2D_BF16 = 1,
+    SS2D_E4M3 = 2 /* ss2d_rms_norm's y only */
+} ss2d_dtype;
 
 /* Layouts of the fused core's x and y. */
 typedef enum { SS2D_CHANNELS_FIRST = 0, SS2D_CHANNELS_LAST = 1 } ss2d_layout;
@@ -394,6 +398,131 @@ int ss2d_block_device_status(const ss2d_block_args *args, const void *workspace,
  * ss2d_device_status report SS2D_ERR_DEVICE from a context that stays usable.  Enqueued on
  * `stream`; returns SS2D_ERR_INVALID_ARG for a NULL word or a limit out of range. */
 int ss2d_diag_bounded_wait(int *error_word, long long spin_limit, void *stream);
+
+/* ---- Operators of a linear-attention layer as it is served -----------------------------
+ * A norm that adds the residual, a matrix product in 8-bit floating point, and linear
+ * attention with a decay for each head over prompts and for single tokens.  They chain:
+ * ss2d_rms_norm's e4m3 output and scales are ss2d_matmul_fp8's activations, the columns of
+ * its output are ss2d_linear_attention's q, k and v (strided), and ss2d_rms_norm takes what
+ * either writes.  They come without a change to the structs above, so ss2d_version() stays
+ * 107; a caller that must run with a library without them looks the symbols up. */
+
+/* Root-mean-square norm with the residual's addition, for each of `rows` rows of D columns:
+ *   r = x + residual                                        (x alone without a residual)
+ *   y = r / sqrt(mean over D(r^2) + eps) * weight
+ *   residual_out = r, rounded to the residual's type
+ * r and y are fp32 within the call; the norm is of the unrounded r.
+ * x        : (rows, D), SS2D_F32 or SS2D_BF16.
+ * residual : (rows, D), SS2D_F32 or SS2D_BF16, or NULL (then residual_out is NULL too).
+ * weight   : (D) fp32.            eps : 0 .. 1.
+ * y        : (rows, D) SS2D_F32, SS2D_BF16 or SS2D_E4M3.
+ * scales   : (rows, ceil(D / 128)) fp32 with an SS2D_E4M3 y, else NULL.  Each 128 columns of a
+ *            row (the last group may have fewer) share s = max(max|y| / 448, 2^-100), and y
+ *            holds y / s rounded to e4m3 (nearest, ties to even): s times it stands for y.  A
+ *            NaN becomes e4m3's NaN and does not enter the maximum.
+ * residual_out : (rows, D) of the residual's type; may be `residual` itself (in place).
+ * D up to 32768 (16-byte accesses where D is a multiple of 8).  Deterministic. */
+int ss2d_rms_norm(const void *x, int x_dtype, const void *residual, int residual_dtype, const float *weight, float eps,
+                  void *y, int y_dtype, float *scales, void *residual_out, long long rows, int D, void *stream);
+
+/* Matrix product of e4m3 matrices with a scale for each block of 128:
+ *   c[m, n] = sum_kb a_scales[m, kb] * w_scales[n / 128, kb] * sum_{k in block kb} a[m, k] w[n, k]
+ *             (+ bias[n])
+ * with fp32 sums on the tensor cores, block kb being columns 128 kb .. 128 kb + 127 of a and w.
+ * Set struct_size = sizeof(ss2d_matmul_fp8_args).  K must be a multiple of 16; M, N any. */
+typedef struct ss2d_matmul_fp8_args {
+    size_t struct_size;
+    int M, N, K;
+    const void *a;          /* (M, K) e4m3, the activations */
+    const float *a_scales;  /* (M, ceil(K / 128)) fp32: one for each 128 columns of a row */
+    const void *w;          /* (N, K) e4m3, the weights */
+    const float *w_scales;  /* (ceil(N / 128), ceil(K / 128)) fp32: one for each 128 x 128 block */
+    const float *bias;      /* (N) fp32, or NULL */
+    void *c;                /* (M, N) of type c_dtype */
+    int c_dtype;            /* SS2D_F32 or SS2D_BF16 */
+} ss2d_matmul_fp8_args;
+
+/* Bytes of device workspace ss2d_matmul_fp8 needs, or (size_t)-1 if the arguments are invalid
+ * (the pointers are not read). */
+size_t ss2d_matmul_fp8_workspace(const ss2d_matmul_fp8_args *args);
+
+/* The product above.  workspace: at least ss2d_matmul_fp8_workspace(args) bytes, 16-byte
+ * aligned, not overlapping a tensor, not shared by calls that overlap on the GPU; contents need
+ * not be initialised.  Deterministic. */
+int ss2d_matmul_fp8(const ss2d_matmul_fp8_args *args, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Causal linear attention with a decay for each head, over whole sequences.  For each sequence
+ * b and head h, with a state S (Dk, Dv), S = h0[b, h] before the first token:
+ *   S   <- exp(log_decay) S + k_t v_t^T
+ *   o_t  = scale * S^T q_t
+ * Heads share q and k in groups, as ss2d_selective_scan's channels share Bm and Cm: head h uses
+ * q and k of group h / (H / G).
+ * Set struct_size = sizeof(ss2d_linear_attention_args).  q, k and v are bf16 with dense last
+ * dimensions and any positive strides that are multiples of 8 elements (columns of one
+ * projection's output, for instance); every other tensor is dense. */
+typedef struct ss2d_linear_attention_args {
+    size_t struct_size;
+    int B, L;               /* sequences and tokens of each */
+    int G, H;               /* groups of q and k, and heads: H a multiple of G */
+    int Dk, Dv;             /* widths of q and k, and of v: multiples of 8, 8 .. 128 */
+    const void *q;          /* (B, L, G, Dk) bf16 */
+    const void *k;          /* (B, L, G, Dk) bf16 */
+    const void *v;          /* (B, L, H, Dv) bf16 */
+    long long q_stride[3];  /* strides in elements of q's batch, token and group dimensions; that of */
+    long long k_stride[3];  /* a dimension of one element is not read */
+    long long v_stride[3];  /* batch, token and head of v */
+    const float *log_decay; /* (H) fp32, or (B, L, H) with decay_per_token; at most 0 */
+    int decay_per_token;
+    const int *lengths;     /* (B) int32 in device memory, or NULL: sequence b has lengths[b] tokens (held
+                               within 0 .. L).  The rows of out behind them are left as they were, and
+                               what q, k, v and log_decay hold there is not used. */
+    float scale;
+    const float *h0;        /* (B, H, Dk, Dv) fp32, or NULL for zero */
+    float *h_last;          /* (B, H, Dk, Dv) fp32, or NULL: the state after the last token (h0, or zero,
+                               for a sequence of none); may be h0 itself (in place) */
+    void *out;              /* (B, L, H, Dv) bf16 */
+} ss2d_linear_attention_args;
+
+/* Bytes of device workspace ss2d_linear_attention needs, or (size_t)-1 if the sizes are
+ * invalid (the pointers and strides are not read). */
+size_t ss2d_linear_attention_workspace(const ss2d_linear_attention_args *args);
+
+/* The attention above.  workspace: as for ss2d_matmul_fp8.
+ * Log decays below -128 count as -128 (a decay of zero in fp32), so -infinity resets the state.
+ * The state and the sums are fp32; q, k, v and out are bf16.  Deterministic. */
+int ss2d_linear_attention(const ss2d_linear_attention_args *args, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+/* The same recurrence for one new token of each of B rows, on a pool of states that is updated in
+ * place.  Set struct_size = sizeof(ss2d_linear_attention_step_args). */
+typedef struct ss2d_linear_attention_step_args {
+    size_t struct_size;
+    int B;                  /* rows */
+    int pool;               /* states in the pool */
+    int G, H, Dk, Dv;       /* as for ss2d_linear_attention */
+    const void *q;          /* (B, G, Dk) bf16 */
+    const void *k;          /* (B, G, Dk) bf16 */
+    const void *v;          /* (B, H, Dv) bf16 */
+    long long q_stride[2];  /* strides in elements of q's row and group dimensions, as above */
+    long long k_stride[2];
+    long long v_stride[2];
+    const float *log_decay; /* (H) fp32, or (B, H) with decay_per_token; at most 0 */
+    int decay_per_token;
+    const int *slots;       /* (B) int32 in device memory: the state of row b; a row whose slot is not within
+                               0 .. pool - 1 is empty, and its row of out is left as it was.  Rows of one
+                               slot are consecutive tokens of one sequence, in the order of the rows.
+                               NULL: row b has state b (pool >= B). */
+    float scale;
+    float *state;           /* (pool, H, Dk, Dv) fp32, updated in place */
+    void *out;              /* (B, H, Dv) bf16 */
+} ss2d_linear_attention_step_args;
+
+int ss2d_linear_attention_step(const ss2d_linear_attention_step_args *args, void *stream);
+
+/* Device-side status of the last ss2d_matmul_fp8 or ss2d_linear_attention on this workspace:
+ * SS2D_OK, or SS2D_ERR_DEVICE if a bounded wait of a tensor-core kernel ran out, in which case
+ * that call's outputs are not valid.  Synchronises `stream`. */
+int ss2d_workspace_status(const void *workspace, void *stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,166 @@
+// linear_recurrent.cu -- linear attention token by token (ss2d_linear_attention_step, and short
+// prompts of ss2d_linear_attention).
+//
+//   S <- exp(g) S + k v^T          S (Dk, Dv) fp32 for each sequence and head
+//   o  = scale * S^T q             rounded to bf16
+//
+// One token reads and writes the whole state and does two multiply-adds for each of its
+// elements, so the kernel is bounded by the state's bytes.  A CTA holds 32 columns of one
+// head's state in registers: 8 lanes of 4 columns (16-byte accesses, a 128-byte run for each
+// row of the state) by 16 rows at a time, so that even one sequence of few heads spreads over
+// many SMs, and all of the state's loads are in flight at once.  Columns of the state do not
+// meet: o's column j needs column j of S alone.
+#include "linear_attention.h"
+
+namespace ss2d {
+namespace {
+
+constexpr int kLrThreads = 128;
+constexpr int kLrCols = 32;                       // columns of the state in one CTA
+constexpr int kLrGroups = kLrThreads / (kLrCols / 4);  // rows of the state held by the CTA at a time
+constexpr int kLrRows = kLaMaxDim / kLrGroups;    // rows of the state held by one thread
+
+// STEP: the tokens of this CTA are the rows of the batch that name its slot, in their order (one,
+// where no slot is named twice; the CTAs of the later ones have nothing to do).  Otherwise they
+// are the tokens of sequence b.
+template <bool STEP>
+__global__ void __launch_bounds__(kLrThreads) linear_recurrent_kernel(const LinAttnArgs a)
+{
+    __shared__ float sq[kLaMaxDim], sk[kLaMaxDim];
+    __shared__ float part[kLrThreads / 32][kLrCols];
+    __shared__ int next_row;
+    const int tid = threadIdx.x, lane = tid % 32;
+    const int slices = (a.Dv + kLrCols - 1) / kLrCols;
+    const int slice = (int)(blockIdx.x % slices);
+    const long long bh = blockIdx.x / slices;
+    const int h = (int)(bh % a.H), b = (int)(bh / a.H);
+    const int group = h / (a.H / a.G);
+    const int c = slice * kLrCols + (tid % (kLrCols / 4)) * 4;  // this thread's first column
+    const int r0 = tid / (kLrCols / 4);                         // and first row
+    const bool cols = c < a.Dv;
+
+    if (!STEP && blockIdx.x == 0 && tid == 0)
+        *a.err = 0;  // nothing here waits
+    long long slot = b;
+    int count = a.L;
+    if (STEP) {
+        if (a.slots) {
+            slot = a.slots[b];
+            if (slot < 0 || slot >= a.pool)
+                return;
+            bool earlier = false;
+            for (int i = tid; i < b; i += kLrThreads)
+                earlier |= a.slots[i] == (int)slot;
+            if (__syncthreads_or(earlier))
+                return;
+        }
+    } else if (a.lengths) {
+        count = min(max(a.lengths[b], 0), a.L);
+    }
+
+    const size_t at = ((size_t)slot * a.H + h) * (size_t)a.Dk * a.Dv;
+    float4 s[kLrRows];
+#pragma unroll
+    for (int i = 0; i < kLrRows; ++i) {
+        const int r = r0 + i * kLrGroups;
+        s[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (a.h0 && cols && r < a.Dk)
+            s[i] = *reinterpret_cast<const float4 *>(a.h0 + at + (size_t)r * a.Dv + c);
+    }
+
+    int row = STEP ? b : 0;
+    while (STEP || row < count) {
+        const long long rb = STEP ? row : b, rt = STEP ? 0 : row;
+        if (tid < a.Dk) {
+            sq[tid] = __bfloat162float(a.q[rb * a.q_batch + rt * a.q_token + group * a.q_head + tid]) * a.scale;
+            sk[tid] = __bfloat162float(a.k[rb * a.k_batch + rt * a.k_token + group * a.k_head + tid]);
+        }
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (cols) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(a.v + rb * a.v_batch + rt * a.v_token + h * a.v_head + c);
+            v = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                            __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+        }
+        const float g = a.log_decay[a.per_token ? (rb * (STEP ? 1 : a.L) + rt) * a.H + h : h];
+        const float decay = expf(la_clamp(g));
+        if (STEP && a.slots && tid == 0)
+            next_row = a.B;
+        __syncthreads();
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < kLrRows; ++i) {
+            const int r = r0 + i * kLrGroups;
+            if (r < a.Dk) {
+                const float kr = sk[r], qr = sq[r];
+                s[i].x = fmaf(s[i].x, decay, kr * v.x);
+                s[i].y = fmaf(s[i].y, decay, kr * v.y);
+                s[i].z = fmaf(s[i].z, decay, kr * v.z);
+                s[i].w = fmaf(s[i].w, decay, kr * v.w);
+                o.x = fmaf(qr, s[i].x, o.x);
+                o.y = fmaf(qr, s[i].y, o.y);
+                o.z = fmaf(qr, s[i].z, o.z);
+                o.w = fmaf(qr, s[i].w, o.w);
+            }
+        }
+        // the four rows of a warp, then the warps
+#pragma unroll
+        for (int d = 8; d < 32; d *= 2) {
+            o.x += __shfl_xor_sync(0xffffffffu, o.x, d);
+            o.y += __shfl_xor_sync(0xffffffffu, o.y, d);
+            o.z += __shfl_xor_sync(0xffffffffu, o.z, d);
+            o.w += __shfl_xor_sync(0xffffffffu, o.w, d);
+        }
+        if (lane < kLrCols / 4)
+            *reinterpret_cast<float4 *>(&part[tid / 32][lane * 4]) = o;
+        if (STEP && a.slots) {
+            int next = a.B;
+            for (int i = row + 1 + tid; i < a.B; i += kLrThreads)
+                if (a.slots[i] == (int)slot) {
+                    next = i;
+                    break;
+                }
+            if (next < a.B)
+                atomicMin(&next_row, next);
+        }
+        __syncthreads();
+        if (tid < kLrCols && slice * kLrCols + tid < a.Dv) {
+            float y = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kLrThreads / 32; ++w)
+                y += part[w][tid];
+            a.out[((rb * (STEP ? 1 : a.L) + rt) * a.H + h) * a.Dv + slice * kLrCols + tid] = __float2bfloat16_rn(y);
+        }
+        if (STEP) {
+            if (!a.slots || next_row >= a.B)
+                break;
+            row = next_row;
+            __syncthreads();
+        } else {
+            ++row;
+        }
+    }
+    if (a.h_last && cols) {
+#pragma unroll
+        for (int i = 0; i < kLrRows; ++i) {
+            const int r = r0 + i * kLrGroups;
+            if (r < a.Dk)
+                *reinterpret_cast<float4 *>(a.h_last + at + (size_t)r * a.Dv + c) = s[i];
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_linear_recurrent(const LinAttnArgs &a, bool step, cudaStream_t s)
+{
+    const long long grid = (long long)a.B * a.H * ((a.Dv + kLrCols - 1) / kLrCols);
+    if (grid > 0x7fffffffLL)
+        return cudaErrorInvalidConfiguration;
+    if (step)
+        linear_recurrent_kernel<true><<<(unsigned)grid, kLrThreads, 0, s>>>(a);
+    else
+        linear_recurrent_kernel<false><<<(unsigned)grid, kLrThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace ss2d
