@@ -1,60 +1,578 @@
 // matmul_fp8.cu -- e4m3 matrix product with a scale for each block of 128 (ss2d_matmul_fp8).
 //
-//   c[m, n] = sum_kb a_scales[m, kb] w_scales[n / 128, kb] sum_{k in kb} a[m, k] w[n, k] (+ bias[n])
+//   c[m, n] = sum_kb a_scales[m, kb] w_scales[n / 128, kb] P_kb[m, n] (+ bias[n])
+//   P_kb[m, n] = sum_{k in block kb} a[m, k] w[n, k]
 //
-// with kb the blocks of 128 columns of a and w, all sums in fp32.
+// The scales change from block to block of K, so a block's partial product P_kb cannot stay in the
+// tensor cores' accumulator: tcgen05.mma (kind::f8f6f4, K = 32, four for a block) writes each P_kb
+// into a fresh buffer of tensor memory, and warps of the CTA read it back, scale it and add it
+// to fp32 sums in their registers while the next block's MMAs fill the next buffer.  TMA brings
+// 128 x 128-byte tiles (one block of K) through a ring of stages.
+//
+// Two kernels, by which side of the MMA the tokens are on:
+//   wide_kernel   tokens along the 128 lanes, BN weight rows along the columns; persistent CTAs
+//                 walk the tiles.  A thread's row has one activation scale and its columns one weight
+//                 scale for a block, so a partial product costs one multiply-add.
+//   narrow_kernel weight rows along the 128 lanes, few tokens along the columns, and K split over
+//                 the CTAs of a cluster, which add up in distributed shared memory: the weights' bytes
+//                 bound a product with few tokens, and this spreads their reading over all SMs.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <stddef.h>
 #include <stdint.h>
 
 #include "api_internal.h"
+#include "launch_util.h"
 #include "op_check.h"
 #include "ss2d.h"
+#include "tma.cuh"
 
 namespace ss2d {
 namespace {
 
-constexpr int kFmBlock = 128;
+constexpr int kFmBlock = 128;            // K (in bytes) of a block, a stage and a swizzled row
+constexpr int kFmRows = 128;             // lanes of an MMA
+constexpr uint32_t kFmTile = kFmRows * kFmBlock;  // bytes of a 128-row tile of a stage
+constexpr size_t kFmWorkspace = 256;     // the error word of the bounded waits
 
 struct Fp8Args {
-    const uint8_t *a, *w;
     const float *a_scales, *w_scales, *bias;
     void *c;
     int *err;
-    int M, N, K, KB, c_bf16;
+    int M, N, KB;
+    int c_bf16;
+    int vec;      // wide: bytes that rows of c and their tiles are aligned to: 32, 16 or 0
+    int mtiles;   // wide: tiles along M;  narrow: tiles along the tokens
+    int tiles;    // of the whole product
+    int split;    // narrow: CTAs of a cluster
 };
 
-__device__ __forceinline__ float fm_value(uint8_t v)
+// kind::f8f6f4: fp32 accumulate, e4m3 A and B, both K-major
+__host__ __device__ constexpr uint32_t fm_idesc(int n)
 {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(v, __NV_E4M3)));
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kFmRows >> 4) << 24);
 }
 
-__global__ void __launch_bounds__(256) matmul_fp8_kernel(const Fp8Args p)
+__device__ __forceinline__ uint32_t fm_pack(float lo, float hi)
 {
-    const int m = blockIdx.y * 16 + threadIdx.y, n = blockIdx.x * 16 + threadIdx.x;
-    if (m == 0 && n == 0)
-        *p.err = 0;  // no wait to run out here
-    if (m >= p.M || n >= p.N)
-        return;
-    float acc = 0.0f;
-    for (int kb = 0; kb < p.KB; ++kb) {
-        float part = 0.0f;
-        const int end = min(p.K, (kb + 1) * kFmBlock);
-        for (int k = kb * kFmBlock; k < end; ++k)
-            part = fmaf(fm_value(p.a[(size_t)m * p.K + k]), fm_value(p.w[(size_t)n * p.K + k]), part);
-        acc = fmaf(part, p.a_scales[(size_t)m * p.KB + kb] * p.w_scales[(size_t)(n / kFmBlock) * p.KB + kb], acc);
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+__device__ __forceinline__ void fm_store32(void *p, const uint32_t (&w)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// The block of K that `it` counts, over a ring of n slots: its slot, and the parity of its round.
+struct Ring {
+    uint32_t slot, round;
+    __device__ __forceinline__ Ring(uint32_t it, uint32_t n) : slot(it % n), round((it / n) & 1u) {}
+};
+
+// One block's MMAs: A 128 rows, B n rows, 128 bytes of K.
+__device__ __forceinline__ void fm_mma_block(uint32_t tmem, uint32_t a, uint32_t b, uint32_t idesc)
+{
+#pragma unroll
+    for (uint32_t k = 0; k < kFmBlock / 32; ++k)
+        tc::mma_e4m3(tmem, tc::swizzled_desc(a + 32 * k, 16, 1024), tc::swizzled_desc(b + 32 * k, 16, 1024), idesc, k > 0);
+}
+
+// ---- wide ----------------------------------------------------------------------------------
+
+constexpr int kWideThreads = 320;  // copy warp, MMA warp, eight warps that scale and add
+constexpr int kWideSumThreads = 256;
+
+template <int BN>
+struct Wide {
+    static constexpr int kStages = BN == 256 ? 4 : 6;
+    static constexpr int kBuffers = 512 / BN;                 // of tensor memory
+    static constexpr uint32_t kStage = kFmTile + BN * kFmBlock;
+    static constexpr int kCols = BN / 2;                      // columns of one summing thread
+    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + (2 * kStages + 2 * kBuffers) * 8 + 16;
+};
+
+template <int BN>
+__global__ void __launch_bounds__(kWideThreads, 1)
+    matmul_fp8_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w, const Fp8Args p)
+{
+    using W = Wide<BN>;
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t bars = base + W::kStages * W::kStage;
+    auto full = [&](uint32_t s) { return bars + 8 * s; };
+    auto empty = [&](uint32_t s) { return bars + 8 * (W::kStages + s); };
+    auto done = [&](uint32_t b) { return bars + 8 * (2 * W::kStages + b); };
+    auto taken = [&](uint32_t b) { return bars + 8 * (2 * W::kStages + W::kBuffers + b); };
+    __shared__ uint32_t tmem_slot;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < W::kStages; ++s) {
+            tc::mbar_init(full(s), 1);
+            tc::mbar_init(empty(s), 1);
+        }
+        for (int b = 0; b < W::kBuffers; ++b) {
+            tc::mbar_init(done(b), 1);
+            tc::mbar_init(taken(b), kWideSumThreads / 32);
+        }
+        tc::mbar_init_fence();
+        tc::tma_prefetch_map(&map_a);
+        tc::tma_prefetch_map(&map_w);
+        if (blockIdx.x == 0)
+            *p.err = 0;  // long before any wait of this call can run out
     }
-    if (p.bias)
-        acc += p.bias[n];
-    const size_t at = (size_t)m * p.N + n;
-    if (p.c_bf16)
-        static_cast<__nv_bfloat16 *>(p.c)[at] = __float2bfloat16_rn(acc);
-    else
-        static_cast<float *>(p.c)[at] = acc;
+    if (warp == 1)
+        tc::tmem_alloc(&tmem_slot, 512);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = tmem_slot;
+    bool good = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            for (int tile = blockIdx.x; tile < p.tiles && good; tile += gridDim.x) {
+                const int m0 = tile % p.mtiles * kFmRows, n0 = tile / p.mtiles * BN;
+                for (int kb = 0; kb < p.KB && good; ++kb, ++it) {
+                    const Ring r(it, W::kStages);
+                    good = tc::mbar_wait(empty(r.slot), r.round ^ 1u);
+                    if (!good)
+                        break;
+                    const uint32_t a = base + r.slot * W::kStage;
+                    tc::mbar_expect(full(r.slot), W::kStage);
+                    tc::tma_load_2d(a, &map_a, full(r.slot), kb * kFmBlock, m0);
+                    tc::tma_load_2d(a + kFmTile, &map_w, full(r.slot), kb * kFmBlock, n0);
+                }
+            }
+            // copies must have landed before the CTA's shared memory goes
+            for (uint32_t i = it > W::kStages ? it - W::kStages : 0; i < it; ++i)
+                tc::mbar_wait(full(Ring(i, W::kStages).slot), Ring(i, W::kStages).round);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            for (int tile = blockIdx.x; tile < p.tiles && good; tile += gridDim.x)
+                for (int kb = 0; kb < p.KB && good; ++kb, ++it) {
+                    const Ring r(it, W::kStages), t(it, W::kBuffers);
+                    good = tc::mbar_wait(taken(t.slot), t.round ^ 1u) && tc::mbar_wait(full(r.slot), r.round);
+                    if (!good)
+                        break;
+                    tc::fence_after();
+                    const uint32_t a = base + r.slot * W::kStage;
+                    fm_mma_block(tmem + t.slot * BN, a, a + kFmTile, fm_idesc(BN));
+                    tc::commit(empty(r.slot));
+                    tc::commit(done(t.slot));
+                }
+        }
+    } else {
+        const int half = (warp - 2) / 4;  // of the tile's columns
+        const uint32_t lanes = (uint32_t)(warp % 4) * 32;
+        const int row = (int)lanes + lane;
+        uint32_t it = 0;
+        for (int tile = blockIdx.x; tile < p.tiles && good; tile += gridDim.x) {
+            const int m0 = tile % p.mtiles * kFmRows, n0 = tile / p.mtiles * BN + half * W::kCols;
+            const int m = m0 + row;
+            const float *sa = p.a_scales + (size_t)min(m, p.M - 1) * p.KB;
+            const float *sw = p.w_scales + (size_t)(min(n0, p.N - 1) / kFmBlock) * p.KB;
+            float2 acc[W::kCols / 2];
+#pragma unroll
+            for (int i = 0; i < W::kCols / 2; ++i)
+                acc[i] = make_float2(0.0f, 0.0f);
+            float s_a = __ldg(sa), s_w = __ldg(sw);
+            for (int kb = 0; kb < p.KB && good; ++kb, ++it) {
+                const Ring t(it, W::kBuffers);
+                const float s = s_a * s_w;
+                if (kb + 1 < p.KB) {  // the next block's scales, on their way meanwhile
+                    s_a = __ldg(sa + kb + 1);
+                    s_w = __ldg(sw + kb + 1);
+                }
+                good = __all_sync(0xffffffffu, tc::mbar_wait(done(t.slot), t.round));
+                if (!good)
+                    break;
+                tc::fence_after();
+                const uint32_t from = tmem + (lanes << 16) + t.slot * BN + half * W::kCols;
+                const float2 s2 = make_float2(s, s);
+                uint32_t v[2][16];
+                tc::tmem_ld16(from, v[0]);
+#pragma unroll
+                for (int c = 0; c < W::kCols / 16; ++c) {
+                    tc::tmem_wait16(v[c & 1]);
+                    if (c + 1 < W::kCols / 16)
+                        tc::tmem_ld16(from + 16 * (c + 1), v[(c + 1) & 1]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        acc[c * 8 + i] = __ffma2_rn(
+                            make_float2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])), s2,
+                            acc[c * 8 + i]);
+                }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_arrive(taken(t.slot));
+            }
+            if (!good)
+                break;
+            if (m < p.M && n0 < p.N) {
+                const int cols = min(W::kCols, p.N - n0);
+                if (p.bias)
+#pragma unroll
+                    for (int i = 0; i < W::kCols / 2; ++i) {
+                        if (2 * i < cols)
+                            acc[i].x += __ldg(p.bias + n0 + 2 * i);
+                        if (2 * i + 1 < cols)
+                            acc[i].y += __ldg(p.bias + n0 + 2 * i + 1);
+                    }
+                const size_t at = (size_t)m * p.N + n0;
+                if (p.c_bf16) {
+                    __nv_bfloat16 *c = static_cast<__nv_bfloat16 *>(p.c) + at;
+#pragma unroll
+                    for (int i = 0; i < W::kCols / 16; ++i) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            w[j] = fm_pack(acc[8 * i + j].x, acc[8 * i + j].y);
+                        if (p.vec == 32 && 16 * i + 16 <= cols)
+                            fm_store32(c + 16 * i, w);
+                        else if (p.vec && 16 * i + 8 <= cols) {
+                            *reinterpret_cast<uint4 *>(c + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+                            if (16 * i + 16 <= cols)
+                                *reinterpret_cast<uint4 *>(c + 16 * i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                if (16 * i + 2 * j < cols)
+                                    c[16 * i + 2 * j] = __float2bfloat16_rn(acc[8 * i + j].x);
+                                if (16 * i + 2 * j + 1 < cols)
+                                    c[16 * i + 2 * j + 1] = __float2bfloat16_rn(acc[8 * i + j].y);
+                            }
+                        }
+                    }
+                } else {
+                    float *c = static_cast<float *>(p.c) + at;
+#pragma unroll
+                    for (int i = 0; i < W::kCols / 4; ++i) {
+                        if (p.vec && 4 * i + 4 <= cols)
+                            *reinterpret_cast<float4 *>(c + 4 * i) =
+                                make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
+                        else {
+                            const float f[4] = {acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (4 * i + j < cols)
+                                    c[4 * i + j] = f[j];
+                        }
+                    }
+                }
+            }
+        }
+    }
+    if (!good && lane == 0)
+        atomicExch(p.err, 1);
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 1)
+        tc::tmem_free(tmem, 512);
 }
 
-constexpr size_t kFmWorkspace = 256;  // the error word of the bounded waits
+// ---- narrow --------------------------------------------------------------------------------
+
+constexpr int kNarrowThreads = 192;  // copy warp, MMA warp, four warps that scale and add
+constexpr int kNarrowStages = 4;
+constexpr int kNarrowMaxSplit = 8;
+// 128 columns of tensor memory for a CTA and more than a quarter of an SM's shared memory, so that all
+// CTAs that fit an SM can hold their columns at once: the CTAs of a cluster wait for one another, and
+// none may wait for columns that a CTA of another cluster holds.
+constexpr int kNarrowCols = 128;
+
+template <int BT>
+struct Narrow {
+    static constexpr int kBuffers = kNarrowCols / BT;
+    static constexpr uint32_t kStage = kFmTile + BT * kFmBlock;
+    static constexpr size_t kSmem = 1024 + (size_t)kNarrowStages * kStage + 2 * 4 * BT * 4 +
+                                    (2 * kNarrowStages + 2 * kBuffers) * 8 + 16;
+    static_assert(kSmem > 57 * 1024, "more than a quarter of an SM's shared memory");
+    static_assert((size_t)kNarrowStages * kStage >= (size_t)BT * kFmRows * 4, "the sums reuse the stages");
+};
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+
+__device__ __forceinline__ float cluster_ld(uint32_t addr, uint32_t rank)
+{
+    uint32_t remote;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(remote) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(remote) : "memory");
+    return v;
+}
+
+template <int BT>
+__global__ void __launch_bounds__(kNarrowThreads)
+    matmul_fp8_narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w, const Fp8Args p)
+{
+    using W = Narrow<BT>;
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
+    float *const sums = reinterpret_cast<float *>(smem_raw + (base - tc::smem_u32(smem_raw)));  // [BT][128]
+    float *const scales = sums + kNarrowStages * W::kStage / 4;  // [warp][2][BT]
+    const uint32_t bars = base + kNarrowStages * W::kStage + 2 * 4 * BT * 4;
+    auto full = [&](uint32_t s) { return bars + 8 * s; };
+    auto empty = [&](uint32_t s) { return bars + 8 * (kNarrowStages + s); };
+    auto done = [&](uint32_t b) { return bars + 8 * (2 * kNarrowStages + b); };
+    auto taken = [&](uint32_t b) { return bars + 8 * (2 * kNarrowStages + W::kBuffers + b); };
+    __shared__ uint32_t tmem_slot;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = (int)(blockIdx.x % p.split);
+    const int tile = (int)(blockIdx.x / p.split);
+    const int t0 = tile % p.mtiles * BT, n0 = tile / p.mtiles * kFmRows;
+    const int kb0 = (int)((long long)p.KB * rank / p.split), kb1 = (int)((long long)p.KB * (rank + 1) / p.split);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kNarrowStages; ++s) {
+            tc::mbar_init(full(s), 1);
+            tc::mbar_init(empty(s), 1);
+        }
+        for (int b = 0; b < W::kBuffers; ++b) {
+            tc::mbar_init(done(b), 1);
+            tc::mbar_init(taken(b), 4);
+        }
+        tc::mbar_init_fence();
+        if (blockIdx.x == 0)
+            *p.err = 0;
+    }
+    if (warp == 1)
+        tc::tmem_alloc(&tmem_slot, kNarrowCols);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = tmem_slot;
+    bool good = true;
+    float2 acc[BT / 2];
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const Ring r(it, kNarrowStages);
+                good = tc::mbar_wait(empty(r.slot), r.round ^ 1u);
+                if (!good)
+                    break;
+                const uint32_t w = base + r.slot * W::kStage;
+                tc::mbar_expect(full(r.slot), W::kStage);
+                tc::tma_load_2d(w, &map_w, full(r.slot), kb * kFmBlock, n0);
+                tc::tma_load_2d(w + kFmTile, &map_a, full(r.slot), kb * kFmBlock, t0);
+            }
+            // copies must have landed before the CTA's shared memory goes
+            for (uint32_t i = it > kNarrowStages ? it - kNarrowStages : 0; i < it; ++i)
+                tc::mbar_wait(full(Ring(i, kNarrowStages).slot), Ring(i, kNarrowStages).round);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const Ring r(it, kNarrowStages), t(it, W::kBuffers);
+                good = tc::mbar_wait(taken(t.slot), t.round ^ 1u) && tc::mbar_wait(full(r.slot), r.round);
+                if (!good)
+                    break;
+                tc::fence_after();
+                const uint32_t w = base + r.slot * W::kStage;
+                fm_mma_block(tmem + t.slot * BT, w, w + kFmTile, fm_idesc(BT));
+                tc::commit(empty(r.slot));
+                tc::commit(done(t.slot));
+            }
+        }
+    } else {
+        // Each warp keeps its own copy of a block's BT scales, two blocks deep.
+        const uint32_t lanes = (uint32_t)(warp % 4) * 32;
+        float *const mine = scales + (warp - 2) * 2 * BT;
+        const float *sw = p.w_scales + (size_t)(n0 / kFmBlock) * p.KB;
+        constexpr int kPer = (BT + 31) / 32;
+        float next[kPer];
+        auto fetch = [&](int kb) {
+            const float w = __ldg(sw + kb);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                next[i] = lane + 32 * i < BT && t0 + lane + 32 * i < p.M
+                              ? w * __ldg(p.a_scales + (size_t)(t0 + lane + 32 * i) * p.KB + kb)
+                              : 0.0f;
+        };
+#pragma unroll
+        for (int i = 0; i < BT / 2; ++i)
+            acc[i] = make_float2(0.0f, 0.0f);
+        if (kb0 < kb1)
+            fetch(kb0);
+        uint32_t it = 0;
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+            const Ring t(it, W::kBuffers);
+            float *const s = mine + (it & 1) * BT;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (lane + 32 * i < BT)
+                    s[lane + 32 * i] = next[i];
+            if (kb + 1 < kb1)
+                fetch(kb + 1);
+            __syncwarp();
+            good = __all_sync(0xffffffffu, tc::mbar_wait(done(t.slot), t.round));
+            if (!good)
+                break;
+            tc::fence_after();
+            const uint32_t from = tmem + (lanes << 16) + t.slot * BT;
+#pragma unroll
+            for (int c = 0; c < BT / 16; ++c) {
+                uint32_t v[16];
+                tc::tmem_ld16(from + 16 * c, v);
+                tc::tmem_wait16(v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 f = *reinterpret_cast<const float4 *>(s + 16 * c + 4 * i);
+                    acc[c * 8 + 2 * i] = __ffma2_rn(
+                        make_float2(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])), make_float2(f.x, f.y),
+                        acc[c * 8 + 2 * i]);
+                    acc[c * 8 + 2 * i + 1] = __ffma2_rn(
+                        make_float2(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])), make_float2(f.z, f.w),
+                        acc[c * 8 + 2 * i + 1]);
+                }
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0)
+                tc::mbar_arrive(taken(t.slot));
+        }
+    }
+    if (!good && lane == 0)
+        atomicExch(p.err, 1);
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();  // every MMA and copy of this CTA is done: its stages are free
+    if (warp == 1)
+        tc::tmem_free(tmem, kNarrowCols);
+    if (warp >= 2) {
+        const int row = (warp % 4) * 32 + lane;
+#pragma unroll
+        for (int i = 0; i < BT / 2; ++i) {
+            sums[(2 * i) * kFmRows + row] = acc[i].x;
+            sums[(2 * i + 1) * kFmRows + row] = acc[i].y;
+        }
+    }
+    // The cluster's CTAs add their parts of K in rank order, each for its share of the tokens.
+    if (p.split > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    if (warp >= 2) {
+        const int row = (warp % 4) * 32 + lane, n = n0 + row;
+        const float bias = p.bias && n < p.N ? __ldg(p.bias + n) : 0.0f;
+        const int per = BT / p.split;
+        const uint32_t from = base + (uint32_t)row * 4;
+        for (int t = rank * per; t < (rank + 1) * per && t0 + t < p.M; ++t) {
+            float y = 0.0f;
+            if (p.split > 1) {
+                for (int r = 0; r < p.split; ++r)
+                    y += cluster_ld(from + (uint32_t)t * kFmRows * 4, (uint32_t)r);
+            } else {
+                y = sums[t * kFmRows + row];
+            }
+            y += bias;
+            if (n < p.N) {
+                const size_t at = (size_t)(t0 + t) * p.N + n;
+                if (p.c_bf16)
+                    static_cast<__nv_bfloat16 *>(p.c)[at] = __float2bfloat16_rn(y);
+                else
+                    static_cast<float *>(p.c)[at] = y;
+            }
+        }
+    }
+    if (p.split > 1)
+        cluster_sync();  // no CTA leaves while another reads its sums
+}
+
+// ---- host ----------------------------------------------------------------------------------
+
+cudaError_t fm_map(CUtensorMap *map, const void *base, int rows, int K, int box_rows)
+{
+    const cuuint64_t sizes[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)K};
+    const cuuint32_t box[2] = {kFmBlock, (cuuint32_t)box_rows};
+    return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, sizes, strides, box);
+}
+
+template <int BN>
+cudaError_t launch_wide(const ss2d_matmul_fp8_args &g, Fp8Args p, int sms, cudaStream_t s)
+{
+    static int configured[kMaxDevices];
+    CUtensorMap a, w;
+    cudaError_t e = fm_map(&a, g.a, g.M, g.K, kFmRows);
+    if (e == cudaSuccess)
+        e = fm_map(&w, g.w, g.N, g.K, BN);
+    if (e == cudaSuccess)
+        e = configure_smem(matmul_fp8_wide_kernel<BN>, (int)Wide<BN>::kSmem, configured);
+    if (e != cudaSuccess)
+        return e;
+    p.mtiles = (g.M + kFmRows - 1) / kFmRows;
+    const long long tiles = (long long)p.mtiles * ((g.N + BN - 1) / BN);
+    if (tiles > 0x7fffffff - sms)
+        return cudaErrorInvalidConfiguration;
+    p.tiles = (int)tiles;
+    matmul_fp8_wide_kernel<BN><<<min(p.tiles, sms), kWideThreads, Wide<BN>::kSmem, s>>>(a, w, p);
+    return cudaGetLastError();
+}
+
+template <int BT>
+cudaError_t launch_narrow(const ss2d_matmul_fp8_args &g, Fp8Args p, int split, cudaStream_t s)
+{
+    static int configured[kMaxDevices];
+    CUtensorMap a, w;
+    cudaError_t e = fm_map(&a, g.a, g.M, g.K, BT);
+    if (e == cudaSuccess)
+        e = fm_map(&w, g.w, g.N, g.K, kFmRows);
+    if (e == cudaSuccess)
+        e = configure_smem(matmul_fp8_narrow_kernel<BT>, (int)Narrow<BT>::kSmem, configured);
+    if (e != cudaSuccess)
+        return e;
+    p.mtiles = (g.M + BT - 1) / BT;
+    p.tiles = p.mtiles * ((g.N + kFmRows - 1) / kFmRows);
+    p.split = split;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(p.tiles * split));
+    cfg.blockDim = dim3(kNarrowThreads);
+    cfg.dynamicSmemBytes = Narrow<BT>::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)split;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, matmul_fp8_narrow_kernel<BT>, a, w, p);
+}
+
+cudaError_t launch_matmul_fp8(const ss2d_matmul_fp8_args &g, const Fp8Args &p, cudaStream_t s)
+{
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess)
+        return e;
+    const long long rows = (g.N + kFmRows - 1) / kFmRows;
+    const int bt = g.M <= 16 ? 16 : g.M <= 32 ? 32 : 64;
+    const long long tiles = rows * ((g.M + bt - 1) / bt);
+    if (tiles <= 2 * sms) {
+        int split = 1;
+        while (split < kNarrowMaxSplit && tiles * split * 2 <= 2 * sms && split * 2 <= p.KB)
+            split *= 2;
+        return bt == 16 ? launch_narrow<16>(g, p, split, s) : bt == 32 ? launch_narrow<32>(g, p, split, s)
+                                                                      : launch_narrow<64>(g, p, split, s);
+    }
+    const long long wide = (long long)((g.M + kFmRows - 1) / kFmRows) * ((g.N + 255) / 256);
+    return wide >= sms ? launch_wide<256>(g, p, sms, s) : launch_wide<128>(g, p, sms, s);
+}
 
 int fm_check(const char *call, const ss2d_matmul_fp8_args *a)
 {
@@ -64,6 +582,8 @@ int fm_check(const char *call, const ss2d_matmul_fp8_args *a)
         return op_fail(SS2D_ERR_INVALID_ARG, "%s: sizes must be positive (M=%d N=%d K=%d)", call, a->M, a->N, a->K);
     if (a->K % 16 != 0)
         return op_fail(SS2D_ERR_UNSUPPORTED, "%s: K=%d is not a multiple of 16", call, a->K);
+    if (a->M > (1 << 30) || a->N > (1 << 30) || a->K > (1 << 30))
+        return op_fail(SS2D_ERR_INVALID_ARG, "%s: problem too large", call);
     if (a->c_dtype != SS2D_F32 && a->c_dtype != SS2D_BF16)
         return op_fail(SS2D_ERR_UNSUPPORTED, "%s: dtype code %d of c must be SS2D_F32 or SS2D_BF16", call, a->c_dtype);
     return SS2D_OK;
@@ -98,14 +618,12 @@ extern "C" int ss2d_matmul_fp8(const ss2d_matmul_fp8_args *args, void *workspace
                          {"w", args->w, N * K},
                          {"w_scales", args->w_scales, (N + kFmBlock - 1) / kFmBlock * KB * 4},
                          {"bias", args->bias, N * 4}};
-    const OpSpan out[] = {{"c", args->c, M * N * (args->c_dtype == SS2D_BF16 ? 2 : 4)},
-                          {"workspace", workspace, kFmWorkspace}};
+    const size_t esize = args->c_dtype == SS2D_BF16 ? 2 : 4;
+    const OpSpan out[] = {{"c", args->c, M * N * esize}, {"workspace", workspace, kFmWorkspace}};
     st = op_check_tensors(call, in, 5, out, 2);
     if (st != SS2D_OK)
         return st;
     Fp8Args p{};
-    p.a = static_cast<const uint8_t *>(args->a);
-    p.w = static_cast<const uint8_t *>(args->w);
     p.a_scales = args->a_scales;
     p.w_scales = args->w_scales;
     p.bias = args->bias;
@@ -113,11 +631,10 @@ extern "C" int ss2d_matmul_fp8(const ss2d_matmul_fp8_args *args, void *workspace
     p.err = static_cast<int *>(workspace);
     p.M = args->M;
     p.N = args->N;
-    p.K = args->K;
     p.KB = (int)KB;
     p.c_bf16 = args->c_dtype == SS2D_BF16;
-    const dim3 grid((unsigned)((N + 15) / 16), (unsigned)((M + 15) / 16));
-    matmul_fp8_kernel<<<grid, dim3(16, 16), 0, static_cast<cudaStream_t>(stream)>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    const uintptr_t along = reinterpret_cast<uintptr_t>(args->c) | (N * esize);
+    p.vec = along % 32 == 0 ? 32 : along % 16 == 0 ? 16 : 0;
+    const cudaError_t e = launch_matmul_fp8(*args, p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SS2D_OK : op_cuda_fail(e, "ss2d_matmul_fp8 launch");
 }
