@@ -47,6 +47,18 @@ int la_check_stride(const char *call, const char *name, long long size, long lon
     return SS2D_OK;
 }
 
+// Sequences that run token by token: with few tokens a chunk of 128 is mostly padding.
+constexpr int kLaRecurrentTokens = 16;
+
+size_t la_workspace(const ss2d_linear_attention_args &a)
+{
+    if (a.L <= kLaRecurrentTokens)
+        return kLaStatusBytes;
+    LinAttnArgs p{};
+    p.B = a.B, p.L = a.L, p.G = a.G, p.H = a.H, p.Dk = a.Dk, p.Dv = a.Dv;
+    return kLaStatusBytes + linear_chunked_workspace(p);
+}
+
 int la_check(const char *call, const ss2d_linear_attention_args *a)
 {
     if (!a || a->struct_size != sizeof(ss2d_linear_attention_args))
@@ -63,7 +75,7 @@ extern "C" size_t ss2d_linear_attention_workspace(const ss2d_linear_attention_ar
     set_last_error(SS2D_OK, "");
     if (la_check("ss2d_linear_attention_workspace", args) != SS2D_OK)
         return (size_t)-1;
-    return kLaStatusBytes;
+    return la_workspace(*args);
 }
 
 extern "C" int ss2d_linear_attention(const ss2d_linear_attention_args *args, void *workspace, size_t workspace_bytes,
@@ -85,7 +97,7 @@ extern "C" int ss2d_linear_attention(const ss2d_linear_attention_args *args, voi
             (st = la_check_stride(call, t.name, a.L, t.s[1])) != SS2D_OK ||
             (st = la_check_stride(call, t.name, t.heads, t.s[2])) != SS2D_OK)
             return st;
-    const size_t need = ss2d_linear_attention_workspace(args);
+    const size_t need = la_workspace(a);
     if (!workspace || workspace_bytes < need)
         return op_fail(SS2D_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", call, need, workspace_bytes);
     const size_t BH = (size_t)a.B * a.H, state = BH * a.Dk * a.Dv * 4;
@@ -117,7 +129,10 @@ extern "C" int ss2d_linear_attention(const ss2d_linear_attention_args *args, voi
     p.err = static_cast<int *>(workspace);
     p.scale = a.scale;
     p.B = a.B, p.L = a.L, p.G = a.G, p.H = a.H, p.Dk = a.Dk, p.Dv = a.Dv;
-    const cudaError_t e = launch_linear_recurrent(p, false, static_cast<cudaStream_t>(stream));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = a.L <= kLaRecurrentTokens
+                              ? launch_linear_recurrent(p, false, s)
+                              : launch_linear_chunked(p, static_cast<char *>(workspace) + kLaStatusBytes, s);
     return e == cudaSuccess ? SS2D_OK : op_cuda_fail(e, "ss2d_linear_attention launch");
 }
 

@@ -37,6 +37,10 @@ struct LinAttnArgs {
     int B, L, G, H, Dk, Dv, pool;
 };
 
+// Token by token.
 cudaError_t launch_linear_recurrent(const LinAttnArgs &a, bool step, cudaStream_t s);
+// In chunks of 128 tokens, with linear_chunked_workspace (of the sizes alone) bytes of workspace.
+size_t linear_chunked_workspace(const LinAttnArgs &a);
+cudaError_t launch_linear_chunked(const LinAttnArgs &a, void *workspace, cudaStream_t s);
 
 }  // namespace ss2d
