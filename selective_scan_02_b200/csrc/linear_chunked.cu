@@ -7,19 +7,22 @@
 //   S'  = exp(c_last) S + sum_j exp(c_last - c_j) k_j v_j^T
 //
 // so a chunk is four products of 128 tokens:  Q K^T,  P V with P the masked and decayed scores,
-// Q S, and K^T (w V) with w_j = exp(c_last - c_j).  A CTA walks the chunks of one head of one
-// sequence (or of one segment of it) with the state in registers:
-//   copy warp    TMA: Q, K and V tiles, each in a ring of two slots
-//   MMA warp     one thread issues tcgen05.mma
+// Q S, and K^T (w V) with w_j = exp(c_last - c_j).  A CTA walks the chunks of 64 columns of one
+// head's state (the columns of v, o and S do not meet) over one sequence or one segment of it.  Only
+// S' = exp(c_last) S + ... is a chain from chunk to chunk, so every step has warps of its own and
+// works on the chunk that is ready for it:
+//   copy warp    TMA: Q, K and V tiles, each in a ring of slots
+//   MMA warps    one thread of one issues the MMAs of the scores and of P V, one thread of the other
+//                those of the state and of Q S
 //   decay warp   c in 64 bits, and from it every factor that the others need in 32
-//   8 warps      scores -> P (bf16, into tensor memory as the A operand of P V);
-//                V -> w V (two bf16 parts, likewise, transposed: the A operand of (w V)^T K);
-//                the state's update, and its bf16 copy in shared memory for the next Q S;
-//                the output
+//   weight warps V -> w V in three bf16 parts, in shared memory
+//   score warps  scores -> P (bf16, in place in tensor memory: the A operand of P V)
+//   state warps  the state, in registers, and its bf16 copy in shared memory for the next Q S
+//   output warps P V and Q S -> o
 //
 // Roundings to bf16, all for an MMA's operands: P and the copy of S once (what they enter, o, is
-// itself rounded to bf16), w V in two parts that together keep 16 bits, because the state is an fp32
-// result and is summed over the whole sequence.  Sums, states and decays are fp32 or wider.
+// itself rounded to bf16); w V in three parts that together keep 24 bits, because the state is an
+// fp32 result and is summed over the whole sequence.  Sums, states and decays are fp32 or wider.
 //
 // The decays within a chunk: columns are cut in blocks of 32, m_b = c at the end of block b.  A score
 // below the diagonal blocks takes exp(c_i - m_b) exp(m_b - c_j), a product of a row's and a column's
@@ -37,10 +40,11 @@ namespace ss2d {
 namespace {
 
 constexpr int kLcChunk = 128;
-constexpr int kLcThreads = 384;       // copy, MMA, decay and an idle warp, then eight computing ones
-constexpr int kLcCompute = 4;         // the first of them
-constexpr int kLcComputeWarps = 8;
+constexpr int kLcCols = 64;           // columns of the state in one CTA
+constexpr int kLcThreads = 1024;      // copy warp, MMA warp, decay warp, the state's MMA warp, then the groups:
+constexpr int kLcWeight = 4, kLcScore = 12, kLcState = 20, kLcOutput = 28;  // their first warps (8, 8, 8 and 4)
 constexpr uint32_t kLcBlock = kLcChunk * 128;  // bytes of 128 tokens by 64 columns of bf16
+constexpr int kLcParts = 3;           // of w V
 constexpr int kLcSms = 148;
 
 // Factors of one chunk's decays, all from 64-bit sums; logarithms to base 2.
@@ -60,24 +64,31 @@ struct ChunkedArgs {
     int nseg, seg_chunks;
 };
 
-template <int DK, int DV>
+template <int DK>
 struct Lc {
+    static constexpr int kSlots = DK == 64 ? 3 : 2;      // of the rings: chunks in flight
     static constexpr uint32_t kQK = DK / 64 * kLcBlock;  // bytes of a tile of Q or K
-    static constexpr uint32_t kV = DV / 64 * kLcBlock;
-    static constexpr uint32_t kS = DK / 64 * DV * 128;   // the bf16 state: DV rows of DK, blocks of 64
-    static constexpr uint32_t kTiles = 2 * (2 * kQK + kV) + kS;
-    static constexpr uint32_t kDecayAt = kTiles;
-    static constexpr uint32_t kBarsAt = kDecayAt + 2 * (uint32_t)sizeof(ChunkDecay);
-    static constexpr size_t kSmem = kBarsAt + 24 * 8;
+    static constexpr uint32_t kS = DK * 128;             // the bf16 state: DK rows of 64 columns
+    static constexpr uint32_t kQAt = 0, kKAt = kQAt + kSlots * kQK, kVAt = kKAt + kSlots * kQK,
+                              kWAt = kVAt + kSlots * kLcBlock, kSAt = kWAt + kLcParts * kLcBlock, kDecayAt = kSAt + kS,
+                              kBarsAt = kDecayAt + kSlots * (uint32_t)sizeof(ChunkDecay);
+    // mbarriers: rings of kSlots, then pairs, then single ones
+    static constexpr int kQkFull = 0, kVFull = kQkFull + kSlots, kQFree = kVFull + kSlots, kKFree = kQFree + kSlots,
+                         kVFree = kKFree + kSlots, kDecFull = kVFree + kSlots, kDecFree = kDecFull + kSlots,
+                         kScoresDone = kDecFree + kSlots, kProbsReady = kScoresDone + 2, kOutDone = kProbsReady + 2,
+                         kOutFree = kOutDone + 2, kWeightsReady = kOutFree + 2, kWeightsFree = kWeightsReady + 2,
+                         kDeltaDone = kWeightsFree + 2, kDeltaFree = kDeltaDone + 1, kStateReady = kDeltaFree + 1,
+                         kInterDone = kStateReady + 1, kInterFree = kInterDone + 1, kBars = kInterFree + 1;
+    static constexpr size_t kSmem = kBarsAt + kBars * 8 + 8;
     static_assert(kSmem <= 232448, "shared memory of an SM");
-    // tensor memory: scores (P in place), output, Q S and then (w V)^T K, the two parts of w V
-    static constexpr uint32_t kScores = 0, kOut = 128, kInter = 256, kHi = 384, kLo = 448;
 };
+// Columns of tensor memory: scores (two buffers; P in place), P V (two), Q S, K^T (w V).
+constexpr uint32_t kLcScoresAt = 0, kLcOutAt = 256, kLcInterAt = 384, kLcDeltaAt = 448;
 
 // kind::f16, fp32 accumulate, bf16 operands, 128 rows
-__host__ __device__ constexpr uint32_t lc_idesc(int n, bool b_mn_major)
+__host__ __device__ constexpr uint32_t lc_idesc(int n, bool a_mn_major, bool b_mn_major)
 {
-    return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+    return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn_major ? 1u << 15 : 0u) | (b_mn_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(128 >> 4) << 24);
 }
 
@@ -102,30 +113,29 @@ __device__ __forceinline__ void lc_store32(void *p, const uint32_t *w)
 }
 
 // STATES: the first pass over segments, which sums their own states alone.
-template <int DK, int DV, bool STATES>
+template <int DK, bool STATES>
 __global__ void __launch_bounds__(kLcThreads, 1)
     linear_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                           const __grid_constant__ CUtensorMap map_v, const ChunkedArgs p)
 {
-    using C = Lc<DK, DV>;
+    using C = Lc<DK>;
     extern __shared__ __align__(1024) unsigned char smem[];
     const LinAttnArgs &a = p.a;
     const uint32_t base = tc::smem_u32(smem);
-    const uint32_t sQ = base, sK = sQ + 2 * C::kQK, sV = sK + 2 * C::kQK, sS = sV + 2 * C::kV;
     ChunkDecay *const decay = reinterpret_cast<ChunkDecay *>(smem + C::kDecayAt);
-    const uint32_t bars = base + C::kBarsAt;
-    const uint32_t q_full = bars, k_full = bars + 16, v_full = bars + 32, q_free = bars + 48, k_free = bars + 64,
-                   v_free = bars + 80, dec_full = bars + 96, dec_free = bars + 112, scores_done = bars + 128,
-                   inter_done = bars + 136, operands = bars + 144, delta_done = bars + 152, out_done = bars + 160,
-                   state_ready = bars + 168;
-    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kBarsAt + 184);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    auto bar = [&](int which) { return base + C::kBarsAt + 8 * (uint32_t)which; };
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kBarsAt + C::kBars * 8);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
 
     const int segs = STATES ? p.nseg - 1 : p.nseg;  // the last segment's own state is not carried on
-    const int seg = (int)(blockIdx.x % segs);
-    const long long bh = blockIdx.x / segs;
+    const int slices = (a.Dv + kLcCols - 1) / kLcCols;
+    const int slice = (int)(blockIdx.x % slices);
+    const int seg = (int)(blockIdx.x / slices % segs);
+    const long long bh = blockIdx.x / slices / segs;
     const int h = (int)(bh % a.H), b = (int)(bh / a.H);
     const int group = h / (a.H / a.G);
+    const int c0 = slice * kLcCols;              // this CTA's columns of v, o and S
+    const int cols = min(kLcCols, a.Dv - c0);    // a multiple of 8
     const int len = a.lengths ? min(max(a.lengths[b], 0), a.L) : a.L;
     const int t_first = seg * p.seg_chunks * kLcChunk;
     const int t_end = min(len, t_first + p.seg_chunks * kLcChunk);
@@ -136,15 +146,28 @@ __global__ void __launch_bounds__(kLcThreads, 1)
     const int chunks = (t_end - t_first + kLcChunk - 1) / kLcChunk;  // 0 for an empty sequence: its state is kept
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            for (uint32_t bar : {q_full, k_full, v_full, q_free, k_free, v_free, dec_full})
-                tc::mbar_init(bar + 8 * i, 1);
-            tc::mbar_init(dec_free + 8 * i, kLcComputeWarps);
+        for (int i = 0; i < C::kSlots; ++i) {
+            tc::mbar_init(bar(C::kQkFull + i), 1);
+            tc::mbar_init(bar(C::kVFull + i), 1);
+            tc::mbar_init(bar(C::kQFree + i), 2);               // the scores and Q S
+            tc::mbar_init(bar(C::kKFree + i), STATES ? 1 : 2);  // the scores and the state
+            tc::mbar_init(bar(C::kVFree + i), STATES ? 8 : 9);  // the weight warps and P V
+            tc::mbar_init(bar(C::kDecFull + i), 1);
+            tc::mbar_init(bar(C::kDecFree + i), STATES ? 16 : 28);  // every warp of the groups
         }
-        for (uint32_t bar : {scores_done, inter_done, delta_done, out_done})
-            tc::mbar_init(bar, 1);
-        tc::mbar_init(operands, kLcComputeWarps);
-        tc::mbar_init(state_ready, kLcComputeWarps);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(bar(C::kScoresDone + i), 1);
+            tc::mbar_init(bar(C::kProbsReady + i), 8);
+            tc::mbar_init(bar(C::kOutDone + i), 1);
+            tc::mbar_init(bar(C::kOutFree + i), 4);
+            tc::mbar_init(bar(C::kWeightsReady + i), 8);
+            tc::mbar_init(bar(C::kWeightsFree + i), 1);
+        }
+        tc::mbar_init(bar(C::kDeltaDone), 1);
+        tc::mbar_init(bar(C::kDeltaFree), 8);
+        tc::mbar_init(bar(C::kStateReady), 8);
+        tc::mbar_init(bar(C::kInterDone), 1);
+        tc::mbar_init(bar(C::kInterFree), 4);
         tc::mbar_init_fence();
     }
     if (warp == 1)
@@ -154,88 +177,147 @@ __global__ void __launch_bounds__(kLcThreads, 1)
     tc::fence_after();
     const uint32_t tmem = *tmem_slot;
     bool good = true;
+    // a warp of a group: waits together
+    auto wait = [&](int which, uint32_t parity) {
+        good = __all_sync(0xffffffffu, tc::mbar_wait(bar(which), parity));
+        tc::fence_after();
+        return good;
+    };
+    auto arrive = [&](int which) {
+        if (lane == 0)
+            tc::mbar_arrive(bar(which));
+    };
+    // one thread
+    auto ready = [&](int which, uint32_t parity) {
+        good = good && tc::mbar_wait(bar(which), parity);
+        tc::fence_after();
+        return good;
+    };
+    const int quarter = warp % 4;                // of the 128 lanes of tensor memory
+    const uint32_t lanes = tmem + ((uint32_t)quarter << 21);
+    const int row = quarter * 32 + lane;
 
     if (warp == 0) {
         if (lane == 0) {
             int issued = 0;
-            for (int c = 0; c < chunks && good; ++c, ++issued) {
-                const uint32_t i = c & 1, round = (c >> 1) & 1;
+            for (int c = 0; c < chunks; ++c, ++issued) {
+                const uint32_t i = c % C::kSlots, round = (c / C::kSlots) & 1;
                 const int t0 = t_first + c * kLcChunk;
-                auto load = [&](uint32_t tile, const CUtensorMap &map, uint32_t full, uint32_t free, int bytes, int head) {
-                    if (!tc::mbar_wait(free + 8 * i, round ^ 1u))
-                        return false;
-                    tc::mbar_expect(full + 8 * i, bytes);
-                    for (int x = 0; x < bytes / (int)kLcBlock; ++x)
-                        tc::tma_load_4d(tile + i * bytes + x * kLcBlock, &map, full + 8 * i, 64 * x, head, t0, b);
-                    return true;
-                };
-                good = load(sK, map_k, k_full, k_free, C::kQK, group);
-                if (good && !STATES)
-                    good = load(sQ, map_q, q_full, q_free, C::kQK, group);
-                if (good)
-                    good = load(sV, map_v, v_full, v_free, C::kV, h);
+                if (!ready(C::kKFree + i, round ^ 1u) || (!STATES && !ready(C::kQFree + i, round ^ 1u)))
+                    break;
+                tc::mbar_expect(bar(C::kQkFull + i), (STATES ? 1 : 2) * C::kQK);
+#pragma unroll
+                for (int x = 0; x < DK / 64; ++x) {
+                    const uint32_t at = i * C::kQK + x * kLcBlock;
+                    tc::tma_load_4d(base + C::kKAt + at, &map_k, bar(C::kQkFull + i), 64 * x, group, t0, b);
+                    if (!STATES)
+                        tc::tma_load_4d(base + C::kQAt + at, &map_q, bar(C::kQkFull + i), 64 * x, group, t0, b);
+                }
+                if (!ready(C::kVFree + i, round ^ 1u)) {
+                    tc::mbar_wait(bar(C::kQkFull + i), round);
+                    break;
+                }
+                tc::mbar_expect(bar(C::kVFull + i), kLcBlock);
+                tc::tma_load_4d(base + C::kVAt + i * kLcBlock, &map_v, bar(C::kVFull + i), c0, h, t0, b);
             }
             // copies must have landed before the CTA's shared memory goes
-            for (int c = max(0, issued - 2); c < issued; ++c)
-                for (uint32_t full : {k_full, q_full, v_full})
-                    if (!STATES || full != q_full)
-                        tc::mbar_wait(full + 8 * (c & 1), (c >> 1) & 1);
-        }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            for (int c = 0; c < chunks && good; ++c) {
-                const uint32_t i = c & 1, round = (c >> 1) & 1, turn = c & 1;
-                const uint32_t tQ = sQ + i * C::kQK, tK = sK + i * C::kQK, tV = sV + i * C::kV;
-                good = tc::mbar_wait(k_full + 8 * i, round) && (STATES || tc::mbar_wait(q_full + 8 * i, round));
-                if (!good)
-                    break;
-                if (!STATES) {
-                    // scores = Q K^T; the P V of the chunk before, which reads P in its place, was issued before
-                    tc::fence_after();
-#pragma unroll
-                    for (int k = 0; k < DK / 16; ++k) {
-                        const uint32_t off = k / 4 * kLcBlock + k % 4 * 32;
-                        tc::mma_bf16(tmem + C::kScores, tc::swizzled_desc(tQ + off, 16, 1024),
-                                     tc::swizzled_desc(tK + off, 16, 1024), lc_idesc(128, false), k > 0);
-                    }
-                    tc::commit(scores_done);
-                    // Q S
-                    good = tc::mbar_wait(state_ready, turn);
-                    if (!good)
-                        break;
-                    tc::fence_after();
-#pragma unroll
-                    for (int k = 0; k < DK / 16; ++k)
-                        tc::mma_bf16(tmem + C::kInter, tc::swizzled_desc(tQ + k / 4 * kLcBlock + k % 4 * 32, 16, 1024),
-                                     tc::swizzled_desc(sS + k / 4 * (DV * 128) + k % 4 * 32, 16, 1024),
-                                     lc_idesc(DV, false), k > 0);
-                    tc::commit(inter_done);
-                    tc::commit(q_free + 8 * i);
-                }
-                good = tc::mbar_wait(v_full + 8 * i, round) && tc::mbar_wait(operands, turn);
-                if (!good)
-                    break;
-                tc::fence_after();
-                // (w V)^T K, the two parts of w V after one another
-#pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                    for (int k = 0; k < kLcChunk / 16; ++k)
-                        tc::mma_bf16_ta(tmem + C::kInter, tmem + (part ? C::kLo : C::kHi) + 8 * k,
-                                        tc::swizzled_desc(tK + 2048 * k, kLcBlock, 1024), lc_idesc(DK, true),
-                                        part > 0 || k > 0);
-                tc::commit(delta_done);
-                tc::commit(k_free + 8 * i);
-                if (!STATES) {
-                    // out += P V; P of tokens 32 b .. lies in the first 16 columns of block b of the scores
-#pragma unroll
-                    for (int k = 0; k < kLcChunk / 16; ++k)
-                        tc::mma_bf16_ta(tmem + C::kOut, tmem + C::kScores + k / 2 * 32 + k % 2 * 8,
-                                        tc::swizzled_desc(tV + 2048 * k, kLcBlock, 1024), lc_idesc(DV, true), 1);
-                    tc::commit(out_done);
-                }
-                tc::commit(v_free + 8 * i);
+            for (int c = max(0, issued - C::kSlots); c < issued; ++c) {
+                tc::mbar_wait(bar(C::kQkFull + c % C::kSlots), (c / C::kSlots) & 1);
+                tc::mbar_wait(bar(C::kVFull + c % C::kSlots), (c / C::kSlots) & 1);
             }
+        }
+    } else if (warp == 1 && !STATES) {
+        // descriptors of the first slot's tiles; an address enters them in units of 16 bytes
+        const uint64_t q_k = tc::swizzled_desc(base + C::kQAt, 16, 1024);         // K-major
+        const uint64_t k_k = tc::swizzled_desc(base + C::kKAt, 16, 1024);
+        const uint64_t v_mn = tc::swizzled_desc(base + C::kVAt, kLcBlock, 1024);  // MN-major
+        auto scores = [&](int c) {
+            // the buffer is free: the P V of two chunks before, which reads P in its place, was issued before
+            const uint32_t i = c % C::kSlots;
+            if (!wait(C::kQkFull + i, (c / C::kSlots) & 1))
+                return;
+            const uint64_t q = q_k + i * (C::kQK / 16), k = k_k + i * (C::kQK / 16);
+            if (tc::elect_one()) {
+#pragma unroll
+                for (int j = 0; j < DK / 16; ++j) {
+                    const uint32_t off = (j / 4 * kLcBlock + j % 4 * 32) / 16;
+                    tc::mma_bf16(tmem + kLcScoresAt + (c & 1) * 128, q + off, k + off, lc_idesc(128, false, false), j > 0);
+                }
+                tc::commit(bar(C::kScoresDone + (c & 1)));
+                tc::commit(bar(C::kQFree + i));
+                tc::commit(bar(C::kKFree + i));
+            }
+            __syncwarp();
+        };
+        if (chunks > 0)
+            scores(0);
+        for (int c = 0; c < chunks && good; ++c) {
+            const uint32_t i = c % C::kSlots, round = (c / C::kSlots) & 1, two = c & 1, turn = (c >> 1) & 1;
+            if (c + 1 < chunks)
+                scores(c + 1);
+            // P V; P of 16 tokens lies in the first 8 of their 16 columns of the scores.  In a chunk that is not
+            // full the weight warps clear the rows of V behind the last token.
+            if (!wait(C::kVFull + i, round) || !wait(C::kProbsReady + two, turn) || !wait(C::kOutFree + two, turn ^ 1u) ||
+                (t_first + (c + 1) * kLcChunk > t_end && !wait(C::kWeightsReady, two)))
+                break;
+            const uint64_t v = v_mn + i * (kLcBlock / 16);
+            if (tc::elect_one()) {
+#pragma unroll
+                for (int j = 0; j < kLcChunk / 16; ++j)
+                    tc::mma_bf16_ta(tmem + kLcOutAt + two * kLcCols, tmem + kLcScoresAt + two * 128 + j * 16,
+                                    v + j * (2048 / 16), lc_idesc(kLcCols, false, true), j > 0);
+                tc::commit(bar(C::kOutDone + two));
+                tc::commit(bar(C::kVFree + i));
+            }
+            __syncwarp();
+        }
+    } else if (warp == 3) {
+        const uint64_t q_k = tc::swizzled_desc(base + C::kQAt, 16, 1024);         // K-major
+        const uint64_t k_mn = tc::swizzled_desc(base + C::kKAt, kLcBlock, 1024);  // MN-major
+        const uint64_t w_mn = tc::swizzled_desc(base + C::kWAt, kLcBlock, 1024);
+        const uint64_t s_mn = tc::swizzled_desc(base + C::kSAt, kLcBlock, 1024);
+        constexpr uint32_t kStep = 2048 / 16;  // 16 tokens (or rows of S) of an MN-major tile
+        for (int c = 0; c < chunks && good; ++c) {
+            const uint32_t i = c % C::kSlots, turn = c & 1;
+            // K^T (w V): lanes are rows of S.  With DK = 64 the upper 64 lanes read what lies behind the tile and
+            // give rows that nobody reads.
+            if (!wait(C::kQkFull + i, (c / C::kSlots) & 1) || !wait(C::kDeltaFree, turn ^ 1u))
+                break;
+            const uint64_t kt = k_mn + i * (C::kQK / 16);
+            for (int half = 0; half < 2 && wait(C::kWeightsReady + half, turn); ++half) {
+                if (tc::elect_one()) {
+#pragma unroll
+                    for (int part = 0; part < kLcParts; ++part)
+#pragma unroll
+                        for (int j = 0; j < kLcChunk / 32; ++j)
+                            tc::mma_bf16(tmem + kLcDeltaAt, kt + (half * 4 + j) * kStep,
+                                         w_mn + part * (kLcBlock / 16) + (half * 4 + j) * kStep,
+                                         lc_idesc(kLcCols, true, true), half > 0 || part > 0 || j > 0);
+                    tc::commit(bar(C::kWeightsFree + half));
+                    if (half) {
+                        tc::commit(bar(C::kDeltaDone));
+                        tc::commit(bar(C::kKFree + i));
+                    }
+                }
+                __syncwarp();
+            }
+            if (!good)
+                break;
+            if (STATES)
+                continue;
+            // Q S
+            if (!wait(C::kStateReady, turn) || !wait(C::kInterFree, turn ^ 1u))
+                break;
+            const uint64_t q = q_k + i * (C::kQK / 16);
+            if (tc::elect_one()) {
+#pragma unroll
+                for (int j = 0; j < DK / 16; ++j)
+                    tc::mma_bf16(tmem + kLcInterAt, q + (j / 4 * kLcBlock + j % 4 * 32) / 16, s_mn + j * kStep,
+                                 lc_idesc(kLcCols, false, true), j > 0);
+                tc::commit(bar(C::kInterDone));
+                tc::commit(bar(C::kQFree + i));
+            }
+            __syncwarp();
         }
     } else if (warp == 2) {
         // Four tokens of each lane, eight lanes of each block.
@@ -252,8 +334,8 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         double whole = 0.0;
         if (chunks > 0)
             fetch(0);
-        for (int c = 0; c < chunks && good; ++c) {
-            const uint32_t i = c & 1, round = (c >> 1) & 1;
+        for (int c = 0; c < chunks; ++c) {
+            const uint32_t i = c % C::kSlots, round = (c / C::kSlots) & 1;
             double s[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -267,23 +349,21 @@ __global__ void __launch_bounds__(kLcThreads, 1)
                 if (lane >= d)
                     before += v;
             }
-            before -= s[3];
-            // an exact zero before the first token, whatever the rounding of the two sums
+            const double end = before;
+            before = __shfl_up_sync(0xffffffffu, before, 1);
             if (lane == 0)
                 before = 0.0;
-            const double end = before + s[3];
             double m[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 m[q] = __shfl_sync(0xffffffffu, end, 8 * q + 7);
-            good = __all_sync(0xffffffffu, tc::mbar_wait(dec_free + 8 * i, round ^ 1u));
-            if (!good)
+            if (!wait(C::kDecFree + i, round ^ 1u))
                 break;
             ChunkDecay &out = decay[i];
             const double mine = lane < 8 ? m[0] : lane < 16 ? m[1] : lane < 24 ? m[2] : m[3];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float cb = (float)(before + s[j] - mine);
+                const float cb = (float)((j < 3 ? before + s[j] : end) - mine);
                 out.cb[lane * 4 + j] = cb;
                 out.f[lane * 4 + j] = exp2f(-cb);
             }
@@ -299,223 +379,246 @@ __global__ void __launch_bounds__(kLcThreads, 1)
             }
             whole += m[3];
             __syncwarp();
-            if (lane == 0)
-                tc::mbar_arrive(dec_full + 8 * i);
+            arrive(C::kDecFull + i);
         }
         if (STATES && lane == 0 && good)
             p.decays[bh * p.nseg + seg] = exp2f((float)whole);
-    } else if (warp >= kLcCompute) {
-        const int quarter = warp % 4, half = (warp - kLcCompute) / 4;
-        const uint32_t lanes = tmem + ((uint32_t)quarter << 21);  // this warp's 32 lanes of tensor memory
-        const int row = quarter * 32 + lane;  // token of the scores and of the output; column of V and of S
-        const bool mine = row < DV && row < a.Dv;
-        constexpr int SK = DK / 2;            // rows of S in this thread
-        float s[SK];
-        const float *from = STATES ? nullptr
-                            : p.nseg > 1 ? p.states + (bh * p.nseg + seg) * (long long)a.Dk * a.Dv
-                            : a.h0       ? a.h0 + bh * (long long)a.Dk * a.Dv
-                                         : nullptr;
-#pragma unroll
-        for (int i = 0; i < SK; ++i) {
-            const int r = half * SK + i;
-            s[i] = from && mine && r < a.Dk ? from[(long long)r * a.Dv + row] : 0.0f;
-        }
-        // the bf16 copy of S: row `row` of 64-column blocks, 16-byte pieces swizzled as TMA would
-        auto publish = [&] {
-            if (row < DV) {
-#pragma unroll
-                for (int x = 0; x < SK / 8; ++x) {
-                    const int r = half * SK + 8 * x;
-                    const uint32_t at = r / 64 * (DV * 128) + row * 128 + (((r % 64 / 8) ^ (row & 7)) << 4);
-                    *reinterpret_cast<uint4 *>(smem + (sS - base) + at) =
-                        make_uint4(lc_pack(s[8 * x], s[8 * x + 1]), lc_pack(s[8 * x + 2], s[8 * x + 3]),
-                                   lc_pack(s[8 * x + 4], s[8 * x + 5]), lc_pack(s[8 * x + 6], s[8 * x + 7]));
-                }
-            }
-            tc::fence_async_proxy();
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0)
-                tc::mbar_arrive(state_ready);
-        };
-        if (!STATES)
-            publish();
-        auto wait = [&](uint32_t bar, uint32_t parity) {
-            good = __all_sync(0xffffffffu, tc::mbar_wait(bar, parity));
-            tc::fence_after();
-            return good;
-        };
-        for (int c = 0; c < chunks; ++c) {
-            const uint32_t i = c & 1, round = (c >> 1) & 1, turn = c & 1;
-            const int t0 = t_first + c * kLcChunk;
-            const int n = min(kLcChunk, t_end - t0);
+    } else if (warp >= kLcWeight && warp < kLcScore) {
+        // V -> w V, 16 bytes at a time: the same place in three tiles.  A part is the upper 16 bits of what the
+        // parts before it leave, so the subtractions are exact and three parts hold all 24 bits.
+        const int t = threadIdx.x - kLcWeight * 32;
+        for (int c = 0; c < chunks && good; ++c) {
+            const uint32_t i = c % C::kSlots, round = (c / C::kSlots) & 1, turn = c & 1;
+            const int n = min(kLcChunk, t_end - t_first - c * kLcChunk);
             const ChunkDecay &d = decay[i];
-            unsigned char *const tileV = smem + (sV - base) + i * C::kV;
-            if (!wait(dec_full + 8 * i, round) || !wait(v_full + 8 * i, round))
+            unsigned char *const tileV = smem + C::kVAt + i * kLcBlock;
+            unsigned char *const tileW = smem + C::kWAt;
+            if (!wait(C::kDecFull + i, round) || !wait(C::kVFull + i, round) || (n < kLcChunk && !wait(C::kQkFull + i, round)))
                 break;
-            // w V, transposed: lane = column of V, tokens in pairs along the columns of tensor memory
-            if (quarter * 32 < DV) {
-                const unsigned char *const col = tileV + row / 64 * kLcBlock + row % 8 * 2;
-                const uint32_t piece = row % 64 / 8;
+            for (int half = 0; half < 2; ++half) {
+                uint4 v[2];
+                float w[2];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const float e = d.e[half * 2 + x];
-                    uint32_t hi[16], lo[16];
-#pragma unroll
-                    for (int y = 0; y < 8; ++y) {
-                        const int t = half * 64 + x * 32 + y * 4;
-                        const float4 f = *reinterpret_cast<const float4 *>(&d.f[t]);
-                        float w[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-                        for (int z = 0; z < 4; ++z) {
-                            const __nv_bfloat16 v = *reinterpret_cast<const __nv_bfloat16 *>(
-                                col + (t + z) * 128 + ((piece ^ ((t + z) & 7)) << 4));
-                            w[z] = t + z < n ? __bfloat162float(v) * (w[z] * e) : 0.0f;
-                        }
-#pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            const uint32_t h2 = lc_pack(w[2 * z], w[2 * z + 1]);
-                            hi[2 * y + z] = h2;
-                            lo[2 * y + z] = lc_pack(w[2 * z] - __uint_as_float(h2 << 16),
-                                                    w[2 * z + 1] - __uint_as_float(h2 & 0xffff0000u));
-                        }
-                    }
-                    tc::tmem_st16(lanes + C::kHi + half * 32 + x * 16, hi);
-                    tc::tmem_st16(lanes + C::kLo + half * 32 + x * 16, lo);
+                    const int at = ((half * 2 + x) * 256 + t) * 16, token = at / 128;
+                    v[x] = *reinterpret_cast<const uint4 *>(tileV + at);
+                    w[x] = d.f[token] * d.e[token / 32];
+                    // a token behind the last: zero, whatever V holds there
+                    if (token >= n)
+                        v[x] = make_uint4(0, 0, 0, 0);
                 }
-            }
-            if (!STATES) {
-                const float cb = d.cb[row];
-                // P: blocks of 32 columns, every other one
-                if (!wait(scores_done, turn))
+                if (!wait(C::kWeightsFree + half, turn ^ 1u))
                     break;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const int blk = 2 * x + half;
-                    uint32_t w[16];
-                    if (blk <= quarter) {
-                        uint32_t v[2][16];
-                        tc::tmem_ld16(lanes + C::kScores + blk * 32, v[0]);
-                        tc::tmem_ld16(lanes + C::kScores + blk * 32 + 16, v[1]);
-                        tc::tmem_wait16(v[0]);
-                        tc::tmem_wait16(v[1]);
-                        if (blk < quarter) {
-                            const float r = a.scale * lc_ex2(cb + d.dm[quarter][blk]);
+                    const int at = ((half * 2 + x) * 256 + t) * 16;
+                    const uint32_t in[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+                    uint32_t part[kLcParts][4];
 #pragma unroll
-                            for (int y = 0; y < 8; ++y) {
-                                const float4 f = *reinterpret_cast<const float4 *>(&d.f[blk * 32 + 4 * y]);
-                                const uint32_t *u = &v[y / 4][y % 4 * 4];
-                                w[2 * y] = lc_pack(__uint_as_float(u[0]) * (f.x * r), __uint_as_float(u[1]) * (f.y * r));
-                                w[2 * y + 1] = lc_pack(__uint_as_float(u[2]) * (f.z * r), __uint_as_float(u[3]) * (f.w * r));
-                            }
-                        } else {
+                    for (int y = 0; y < 4; ++y) {
+                        float2 r = __fmul2_rn(make_float2(__uint_as_float(in[y] << 16), __uint_as_float(in[y] & 0xffff0000u)),
+                                              make_float2(w[x], w[x]));
 #pragma unroll
-                            for (int y = 0; y < 8; ++y) {
-                                const float4 f = *reinterpret_cast<const float4 *>(&d.cb[blk * 32 + 4 * y]);
-                                const uint32_t *u = &v[y / 4][y % 4 * 4];
-                                const float g[4] = {f.x, f.y, f.z, f.w};
-                                float r[4];
-#pragma unroll
-                                for (int z = 0; z < 4; ++z)
-                                    r[z] = 4 * y + z <= lane ? __uint_as_float(u[z]) * (a.scale * lc_ex2(cb - g[z])) : 0.0f;
-                                w[2 * y] = lc_pack(r[0], r[1]);
-                                w[2 * y + 1] = lc_pack(r[2], r[3]);
-                            }
+                        for (int z = 0; z < kLcParts; ++z) {
+                            const uint32_t lo = __float_as_uint(r.x), hi = __float_as_uint(r.y);
+                            part[z][y] = __byte_perm(lo, hi, 0x7632);
+                            r = __fadd2_rn(r, make_float2(__uint_as_float((lo & 0xffff0000u) ^ 0x80000000u),
+                                                          __uint_as_float((hi & 0xffff0000u) ^ 0x80000000u)));
                         }
+                    }
+#pragma unroll
+                    for (int z = 0; z < kLcParts; ++z)
+                        *reinterpret_cast<uint4 *>(tileW + z * kLcBlock + at) =
+                            make_uint4(part[z][0], part[z][1], part[z][2], part[z][3]);
+                }
+                // rows of K and V behind the last token: zero, whatever the tensors hold there, since a factor of
+                // zero would not hide a NaN.  Other warps, and the MMAs of the scores, may still read these rows
+                // as they were: nothing of that reaches a row of the output or the state.
+                if (n < kLcChunk && half == 0)
+                    for (int blk = 0; blk < (STATES ? 0 : 1) + DK / 64; ++blk) {
+                        unsigned char *const tile = blk < DK / 64 ? smem + C::kKAt + i * C::kQK + blk * kLcBlock : tileV;
+                        for (int x = t; x < (kLcChunk - n) * 8; x += 256)
+                            *reinterpret_cast<uint4 *>(tile + n * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                tc::fence_async_proxy();
+                __syncwarp();
+                arrive(C::kWeightsReady + half);
+            }
+            arrive(C::kVFree + i);
+            arrive(C::kDecFree + i);
+        }
+    } else if (warp >= kLcScore && warp < kLcState && !STATES) {
+        const int half = (warp - kLcScore) / 4;  // 16 of a block's 32 columns
+        for (int c = 0; c < chunks; ++c) {
+            const uint32_t i = c % C::kSlots, round = (c / C::kSlots) & 1;
+            const uint32_t two = c & 1, turn2 = (c >> 1) & 1;  // of the scores' two buffers
+            const ChunkDecay &d = decay[i];
+            if (!wait(C::kDecFull + i, round) || !wait(C::kScoresDone + two, turn2))
+                break;
+            const float cb = d.cb[row];
+            const float2 scale2 = make_float2(a.scale, a.scale), cb2 = make_float2(cb, cb);
+#pragma unroll 1
+            for (int blk = 0; blk < 4; ++blk) {
+                const uint32_t at = lanes + kLcScoresAt + two * 128 + blk * 32 + half * 16;
+                uint32_t w[8];
+#pragma unroll
+                for (int y = 0; y < 8; ++y)
+                    w[y] = 0;
+                if (blk <= quarter) {
+                    uint32_t v[16];
+                    tc::tmem_ld16(at, v);
+                    const float4 *const f4 = reinterpret_cast<const float4 *>((blk < quarter ? d.f : d.cb) + blk * 32 + half * 16);
+                    float2 f[8];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const float4 f_ = f4[y];
+                        f[2 * y] = make_float2(f_.x, f_.y), f[2 * y + 1] = make_float2(f_.z, f_.w);
+                    }
+                    if (blk < quarter) {
+                        const float r = a.scale * lc_ex2(cb + d.dm[quarter][blk]);
+#pragma unroll
+                        for (int y = 0; y < 8; ++y)
+                            f[y] = __fmul2_rn(f[y], make_float2(r, r));
                     } else {
 #pragma unroll
-                        for (int y = 0; y < 16; ++y)
-                            w[y] = 0;
+                        for (int y = 0; y < 8; ++y) {
+                            const float2 e = __fadd2_rn(cb2, make_float2(-f[y].x, -f[y].y));
+                            f[y] = __fmul2_rn(scale2, make_float2(lc_ex2(e.x), lc_ex2(e.y)));
+                        }
                     }
-                    tc::tmem_st16(lanes + C::kScores + blk * 32, w);
-                }
-                // what the state gives: the start of the output's sum
-                if (!wait(inter_done, turn))
-                    break;
-                const float r = a.scale * lc_ex2(cb + d.m[quarter]);
-#pragma unroll
-                for (int x = 0; x < DV / 32; ++x) {
-                    uint32_t v[16];
-                    tc::tmem_ld16(lanes + C::kInter + half * (DV / 2) + 16 * x, v);
                     tc::tmem_wait16(v);
 #pragma unroll
-                    for (int y = 0; y < 16; ++y)
-                        v[y] = __float_as_uint(__uint_as_float(v[y]) * r);
-                    tc::tmem_st16(lanes + C::kOut + half * (DV / 2) + 16 * x, v);
-                }
-            }
-            const float total = d.total;
-            // rows of K and V behind the last token: zero, whatever the tensors hold there, since a factor of
-            // zero would not hide a NaN.  Other warps, and the MMAs of the scores, may still read these rows
-            // as they were: nothing of that reaches a row of the output or the state.
-            if (n < kLcChunk) {
-                if (!wait(k_full + 8 * i, round))
-                    break;
-                const int t = threadIdx.x - kLcCompute * 32;
-                auto clear = [&](unsigned char *tile, int blocks) {
-                    for (int x = t; x < blocks * (kLcChunk - n) * 8; x += kLcComputeWarps * 32) {
-                        const int blk = x / ((kLcChunk - n) * 8), at = x % ((kLcChunk - n) * 8);
-                        *reinterpret_cast<uint4 *>(tile + blk * kLcBlock + n * 128 + at * 16) = make_uint4(0, 0, 0, 0);
+                    for (int y = 0; y < 8; ++y) {
+                        const float2 r = __fmul2_rn(f[y], make_float2(__uint_as_float(v[2 * y]), __uint_as_float(v[2 * y + 1])));
+                        w[y] = lc_pack(r.x, r.y);
                     }
-                };
-                clear(smem + (sK - base) + i * C::kQK, DK / 64);
-                clear(tileV, DV / 64);
-                tc::fence_async_proxy();
+                    if (blk == quarter) {
+                        // columns behind the row's own token: none
+                        const int last = lane - half * 16;
+#pragma unroll
+                        for (int y = 0; y < 8; ++y)
+                            w[y] &= (2 * y <= last ? 0xffffu : 0u) | (2 * y + 1 <= last ? 0xffff0000u : 0u);
+                    }
+                }
+                tc::tmem_st8(at, w);
             }
             tc::tmem_wait_st();
             tc::fence_before();
             __syncwarp();
-            if (lane == 0) {
-                tc::mbar_arrive(operands);
-                tc::mbar_arrive(dec_free + 8 * i);
+            arrive(C::kProbsReady + two);
+            arrive(C::kDecFree + i);
+        }
+    } else if (warp >= kLcState && warp < kLcOutput) {
+        const int half = (warp - kLcState) / 4;  // of the columns
+        constexpr int kMine = kLcCols / 2;
+        const bool mine = row < a.Dk;  // row of S
+        const int left = cols - half * kMine;  // columns in this thread, where above 0
+        const long long size = (long long)a.Dk * a.Dv, in_head = (long long)row * a.Dv + c0 + half * kMine;
+        const float *const from = STATES       ? nullptr
+                                  : p.nseg > 1 ? p.states + (bh * p.nseg + seg) * size + in_head
+                                  : a.h0       ? a.h0 + bh * size + in_head
+                                               : nullptr;
+        float2 s[kMine / 2];
+#pragma unroll
+        for (int x = 0; x < kMine; x += 4) {
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (from && mine && x < left)
+                v = *reinterpret_cast<const float4 *>(from + x);
+            s[x / 2] = make_float2(v.x, v.y), s[x / 2 + 1] = make_float2(v.z, v.w);
+        }
+        // the bf16 copy of S, its 16-byte pieces swizzled as TMA would
+        auto publish = [&] {
+            if (row < DK) {
+#pragma unroll
+                for (int x = 0; x < kMine / 8; ++x)
+                    *reinterpret_cast<uint4 *>(smem + C::kSAt + row * 128 + (((half * 4 + x) ^ (row & 7)) << 4)) =
+                        make_uint4(lc_pack(s[4 * x].x, s[4 * x].y), lc_pack(s[4 * x + 1].x, s[4 * x + 1].y),
+                                   lc_pack(s[4 * x + 2].x, s[4 * x + 2].y), lc_pack(s[4 * x + 3].x, s[4 * x + 3].y));
             }
-            if (!wait(delta_done, turn))
+            tc::fence_async_proxy();
+            __syncwarp();
+            arrive(C::kStateReady);
+        };
+        if (!STATES)
+            publish();
+        for (int c = 0; c < chunks; ++c) {
+            const uint32_t i = c % C::kSlots, round = (c / C::kSlots) & 1, turn = c & 1;
+            if (!wait(C::kDecFull + i, round))
+                break;
+            const float2 total = make_float2(decay[i].total, decay[i].total);
+            __syncwarp();
+            arrive(C::kDecFree + i);
+            if (!wait(C::kDeltaDone, turn))
                 break;
 #pragma unroll
-            for (int x = 0; x < SK / 16; ++x) {
+            for (int x = 0; x < kMine / 16; ++x) {
                 uint32_t v[16];
-                tc::tmem_ld16(lanes + C::kInter + half * SK + 16 * x, v);
+                tc::tmem_ld16(lanes + kLcDeltaAt + half * kMine + 16 * x, v);
                 tc::tmem_wait16(v);
 #pragma unroll
-                for (int y = 0; y < 16; ++y)
-                    s[16 * x + y] = fmaf(s[16 * x + y], total, __uint_as_float(v[y]));
+                for (int y = 0; y < 8; ++y)
+                    s[8 * x + y] = __ffma2_rn(s[8 * x + y], total,
+                                              make_float2(__uint_as_float(v[2 * y]), __uint_as_float(v[2 * y + 1])));
             }
+            tc::fence_before();
+            __syncwarp();
+            arrive(C::kDeltaFree);
             if (!STATES) {
-                publish();
-                if (!wait(out_done, turn))
+                // Q S has read the copy that is replaced now
+                if (!wait(C::kInterDone, turn))
                     break;
-                const int t = t0 + row;
-                __nv_bfloat16 *const o = a.out + (((long long)b * a.L + t) * a.H + h) * a.Dv + half * (DV / 2);
-                const bool wide = a.Dv % 16 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
+                publish();
+            }
+        }
+        float *const to = STATES                     ? p.states + (bh * p.nseg + seg) * size + in_head
+                          : a.h_last && t_end == len ? a.h_last + bh * size + in_head
+                                                     : nullptr;
+        if (good && to && mine)
 #pragma unroll
-                for (int x = 0; x < DV / 32; ++x) {
-                    uint32_t v[16], w[8];
-                    tc::tmem_ld16(lanes + C::kOut + half * (DV / 2) + 16 * x, v);
-                    tc::tmem_wait16(v);
+            for (int x = 0; x < kMine; x += 4)
+                if (x < left)
+                    *reinterpret_cast<float4 *>(to + x) = make_float4(s[x / 2].x, s[x / 2].y, s[x / 2 + 1].x, s[x / 2 + 1].y);
+    } else if (warp >= kLcOutput && !STATES) {
+        const bool wide = a.Dv % 16 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
+        for (int c = 0; c < chunks; ++c) {
+            const uint32_t i = c % C::kSlots, round = (c / C::kSlots) & 1, turn = c & 1;
+            const int t = t_first + c * kLcChunk + row;
+            if (!wait(C::kDecFull + i, round))
+                break;
+            const float r = a.scale * lc_ex2(decay[i].cb[row] + decay[i].m[quarter]);
+            __syncwarp();
+            arrive(C::kDecFree + i);
+            if (!wait(C::kInterDone, turn) || !wait(C::kOutDone + (c & 1), (c >> 1) & 1))
+                break;
+            __nv_bfloat16 *const o = a.out + (((long long)b * a.L + t) * a.H + h) * a.Dv + c0;
+#pragma unroll 1
+            for (int x = 0; x < kLcCols / 16; ++x) {
+                uint32_t u[16], v[16], w[8];
+                tc::tmem_ld16(lanes + kLcInterAt + 16 * x, u);
+                tc::tmem_ld16(lanes + kLcOutAt + (c & 1) * kLcCols + 16 * x, v);
+                tc::tmem_wait16(u);
+                tc::tmem_wait16(v);
 #pragma unroll
-                    for (int y = 0; y < 8; ++y)
-                        w[y] = lc_pack(__uint_as_float(v[2 * y]), __uint_as_float(v[2 * y + 1]));
-                    const int left = a.Dv - half * (DV / 2) - 16 * x;  // columns from here on
-                    if (t < t_end && left > 0) {
-                        if (wide) {
-                            lc_store32(o + 16 * x, w);
-                        } else {
-                            *reinterpret_cast<uint4 *>(o + 16 * x) = make_uint4(w[0], w[1], w[2], w[3]);
-                            if (left > 8)
-                                *reinterpret_cast<uint4 *>(o + 16 * x + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-                        }
+                for (int y = 0; y < 8; ++y) {
+                    const float2 z = __ffma2_rn(make_float2(r, r), make_float2(__uint_as_float(u[2 * y]), __uint_as_float(u[2 * y + 1])),
+                                                make_float2(__uint_as_float(v[2 * y]), __uint_as_float(v[2 * y + 1])));
+                    w[y] = lc_pack(z.x, z.y);
+                }
+                if (t < t_end && 16 * x < cols) {
+                    if (wide) {
+                        lc_store32(o + 16 * x, w);
+                    } else {
+                        *reinterpret_cast<uint4 *>(o + 16 * x) = make_uint4(w[0], w[1], w[2], w[3]);
+                        if (16 * x + 8 < cols)
+                            *reinterpret_cast<uint4 *>(o + 16 * x + 8) = make_uint4(w[4], w[5], w[6], w[7]);
                     }
                 }
             }
+            tc::fence_before();
+            __syncwarp();
+            arrive(C::kInterFree);
+            arrive(C::kOutFree + (c & 1));
         }
-        float *const to = STATES                       ? p.states + (bh * p.nseg + seg) * (long long)a.Dk * a.Dv
-                          : a.h_last && t_end == len ? a.h_last + bh * (long long)a.Dk * a.Dv
-                                                       : nullptr;
-        if (good && to && mine)
-#pragma unroll
-            for (int i = 0; i < SK; ++i)
-                if (half * SK + i < a.Dk)
-                    to[(long long)(half * SK + i) * a.Dv + row] = s[i];
     }
     if (!good && lane == 0)
         atomicExch(a.err, 1);
@@ -571,8 +674,8 @@ cudaError_t lc_map(CUtensorMap *map, const __nv_bfloat16 *base, int B, int L, in
     return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, sizes, strides, box);
 }
 
-template <int DK, int DV>
-cudaError_t launch_dims(const ChunkedArgs &p, cudaStream_t s)
+template <int DK>
+cudaError_t launch_width(const ChunkedArgs &p, cudaStream_t s)
 {
     static int configured[2][kMaxDevices];
     const LinAttnArgs &a = p.a;
@@ -583,29 +686,30 @@ cudaError_t launch_dims(const ChunkedArgs &p, cudaStream_t s)
     if (e == cudaSuccess)
         e = lc_map(&v, a.v, a.B, a.L, a.H, a.Dv, a.v_batch, a.v_token, a.v_head);
     if (e == cudaSuccess)
-        e = configure_smem(linear_chunked_kernel<DK, DV, false>, (int)Lc<DK, DV>::kSmem, configured[0]);
+        e = configure_smem(linear_chunked_kernel<DK, false>, (int)Lc<DK>::kSmem, configured[0]);
     if (e != cudaSuccess)
         return e;
-    const long long heads = (long long)a.B * a.H;
+    const long long heads = (long long)a.B * a.H, slices = (a.Dv + kLcCols - 1) / kLcCols;
     if (p.nseg > 1) {
-        e = configure_smem(linear_chunked_kernel<DK, DV, true>, (int)Lc<DK, DV>::kSmem, configured[1]);
+        e = configure_smem(linear_chunked_kernel<DK, true>, (int)Lc<DK>::kSmem, configured[1]);
         if (e != cudaSuccess)
             return e;
-        linear_chunked_kernel<DK, DV, true>
-            <<<(unsigned)(heads * (p.nseg - 1)), kLcThreads, Lc<DK, DV>::kSmem, s>>>(q, k, v, p);
+        linear_chunked_kernel<DK, true>
+            <<<(unsigned)(heads * (p.nseg - 1) * slices), kLcThreads, Lc<DK>::kSmem, s>>>(q, k, v, p);
         const long long per = ((long long)a.Dk * a.Dv + 255) / 256;
         linear_carry_kernel<<<(unsigned)(heads * per), 256, 0, s>>>(p);
     }
-    linear_chunked_kernel<DK, DV, false><<<(unsigned)(heads * p.nseg), kLcThreads, Lc<DK, DV>::kSmem, s>>>(q, k, v, p);
+    linear_chunked_kernel<DK, false>
+        <<<(unsigned)(heads * p.nseg * slices), kLcThreads, Lc<DK>::kSmem, s>>>(q, k, v, p);
     return cudaGetLastError();
 }
 
 // Segments of a sequence: as many as fill the GPU once, of at least four chunks each.
 void lc_plan(const LinAttnArgs &a, int *nseg, int *seg_chunks)
 {
-    const long long heads = (long long)a.B * a.H;
+    const long long units = (long long)a.B * a.H * ((a.Dv + kLcCols - 1) / kLcCols);
     const int chunks = (a.L + kLcChunk - 1) / kLcChunk;
-    long long n = kLcSms / heads;
+    long long n = kLcSms / units;
     n = n < 1 ? 1 : n > chunks / 4 ? (chunks / 4 > 0 ? chunks / 4 : 1) : n;
     *seg_chunks = (int)((chunks + n - 1) / n);
     *nseg = (chunks + *seg_chunks - 1) / *seg_chunks;
@@ -631,15 +735,13 @@ cudaError_t launch_linear_chunked(const LinAttnArgs &a, void *workspace, cudaStr
     p.a = a;
     lc_plan(a, &p.nseg, &p.seg_chunks);
     const long long heads = (long long)a.B * a.H;
-    if (heads * p.nseg > 0x7fffffffLL || heads * 64 > 0x7fffffffLL)
+    if (heads * p.nseg * 2 > 0x7fffffffLL || heads * 64 > 0x7fffffffLL)
         return cudaErrorInvalidConfiguration;
     if (p.nseg > 1) {
         p.decays = static_cast<float *>(workspace);
         p.states = reinterpret_cast<float *>(static_cast<char *>(workspace) + round256((size_t)heads * p.nseg * 4));
     }
-    if (a.Dk <= 64)
-        return a.Dv <= 64 ? launch_dims<64, 64>(p, s) : launch_dims<64, 128>(p, s);
-    return a.Dv <= 64 ? launch_dims<128, 64>(p, s) : launch_dims<128, 128>(p, s);
+    return a.Dk <= 64 ? launch_width<64>(p, s) : launch_width<128>(p, s);
 }
 
 }  // namespace ss2d
