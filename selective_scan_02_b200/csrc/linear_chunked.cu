@@ -14,7 +14,7 @@
 //   copy warp    TMA: Q, K and V tiles, each in a ring of slots
 //   MMA warps    one thread of one issues the MMAs of the scores and of P V, one thread of the other
 //                those of the state and of Q S
-//   decay warp   c in 64 bits, and from it every factor that the others need in 32
+//   decay warp   sums of log decays, and from them every factor that the others need
 //   weight warps V -> w V in three bf16 parts, in shared memory
 //   score warps  scores -> P (bf16, in place in tensor memory: the A operand of P V)
 //   state warps  the state, in registers, and its bf16 copy in shared memory for the next Q S
@@ -45,16 +45,19 @@ constexpr int kLcThreads = 1024;      // copy warp, MMA warp, decay warp, the st
 constexpr int kLcWeight = 4, kLcScore = 12, kLcState = 20, kLcOutput = 28;  // their first warps (8, 8, 8 and 4)
 constexpr uint32_t kLcBlock = kLcChunk * 128;  // bytes of 128 tokens by 64 columns of bf16
 constexpr int kLcParts = 3;           // of w V
+constexpr int kLcIdlePolls = 1 << 25;  // of the copy warp, at 60 ns or more: about 2 s
 constexpr int kLcSms = 148;
 
-// Factors of one chunk's decays, all from 64-bit sums; logarithms to base 2.
+constexpr float kLcLog2e = 1.4426950408889634f, kLcLn2 = 0.6931471805599453f;
+
+// Factors of one chunk's decays; logarithms to base 2.
 struct alignas(16) ChunkDecay {
     float cb[kLcChunk];  // c_j - m_b of j's block
     float f[kLcChunk];   // exp(m_b - c_j)
     float m[4];          // m_b
     float dm[4][4];      // m_q - m_b
     float e[4];          // exp(c_last - m_b)
-    float total;         // exp(c_last)
+    float keep, grow;    // exp(c_last) = keep + grow: 1 and a small number for slow decays, else 0 and itself
 };
 
 struct ChunkedArgs {
@@ -66,24 +69,25 @@ struct ChunkedArgs {
 
 template <int DK>
 struct Lc {
-    static constexpr int kSlots = DK == 64 ? 3 : 2;      // of the rings: chunks in flight
+    static constexpr int kSlots = DK == 64 ? 3 : 2;      // of the rings of tiles: chunks in flight
+    static constexpr int kDecays = DK == 64 ? 4 : 2;     // of the ring of decays
     static constexpr uint32_t kQK = DK / 64 * kLcBlock;  // bytes of a tile of Q or K
     static constexpr uint32_t kS = DK * 128;             // the bf16 state: DK rows of 64 columns
     static constexpr uint32_t kQAt = 0, kKAt = kQAt + kSlots * kQK, kVAt = kKAt + kSlots * kQK,
                               kWAt = kVAt + kSlots * kLcBlock, kSAt = kWAt + kLcParts * kLcBlock, kDecayAt = kSAt + kS,
-                              kBarsAt = kDecayAt + kSlots * (uint32_t)sizeof(ChunkDecay);
+                              kBarsAt = kDecayAt + kDecays * (uint32_t)sizeof(ChunkDecay);
     // mbarriers: rings of kSlots, then pairs, then single ones
-    static constexpr int kQkFull = 0, kVFull = kQkFull + kSlots, kQFree = kVFull + kSlots, kKFree = kQFree + kSlots,
-                         kVFree = kKFree + kSlots, kDecFull = kVFree + kSlots, kDecFree = kDecFull + kSlots,
-                         kScoresDone = kDecFree + kSlots, kProbsReady = kScoresDone + 2, kOutDone = kProbsReady + 2,
-                         kOutFree = kOutDone + 2, kWeightsReady = kOutFree + 2, kWeightsFree = kWeightsReady + 2,
-                         kDeltaDone = kWeightsFree + 2, kDeltaFree = kDeltaDone + 1, kStateReady = kDeltaFree + 1,
+    static constexpr int kQFull = 0, kKFull = kQFull + kSlots, kVFull = kKFull + kSlots, kQFree = kVFull + kSlots, kKFree = kQFree + kSlots,
+                         kVFree = kKFree + kSlots, kDecFull = kVFree + kSlots, kDecFree = kDecFull + kDecays,
+                         kScoresDone = kDecFree + kDecays, kProbsReady = kScoresDone + 2, kWeightsReady = kProbsReady + 2,
+                         kWeightsFree = kWeightsReady + 2, kDeltaDone = kWeightsFree + 2, kDeltaFree = kDeltaDone + 2,
+                         kOutDone = kDeltaFree + 2, kOutFree = kOutDone + 1, kStateReady = kOutFree + 1,
                          kInterDone = kStateReady + 1, kInterFree = kInterDone + 1, kBars = kInterFree + 1;
     static constexpr size_t kSmem = kBarsAt + kBars * 8 + 8;
     static_assert(kSmem <= 232448, "shared memory of an SM");
 };
-// Columns of tensor memory: scores (two buffers; P in place), P V (two), Q S, K^T (w V).
-constexpr uint32_t kLcScoresAt = 0, kLcOutAt = 256, kLcInterAt = 384, kLcDeltaAt = 448;
+// Columns of tensor memory: scores (two buffers; P in place), P V, Q S, K^T (w V) (two).
+constexpr uint32_t kLcScoresAt = 0, kLcOutAt = 256, kLcInterAt = 320, kLcDeltaAt = 384;
 
 // kind::f16, fp32 accumulate, bf16 operands, 128 rows
 __host__ __device__ constexpr uint32_t lc_idesc(int n, bool a_mn_major, bool b_mn_major)
@@ -147,24 +151,27 @@ __global__ void __launch_bounds__(kLcThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
-            tc::mbar_init(bar(C::kQkFull + i), 1);
+            tc::mbar_init(bar(C::kQFull + i), 1);
+            tc::mbar_init(bar(C::kKFull + i), 1);
             tc::mbar_init(bar(C::kVFull + i), 1);
             tc::mbar_init(bar(C::kQFree + i), 2);               // the scores and Q S
             tc::mbar_init(bar(C::kKFree + i), STATES ? 1 : 2);  // the scores and the state
             tc::mbar_init(bar(C::kVFree + i), STATES ? 8 : 9);  // the weight warps and P V
+        }
+        for (int i = 0; i < C::kDecays; ++i) {
             tc::mbar_init(bar(C::kDecFull + i), 1);
             tc::mbar_init(bar(C::kDecFree + i), STATES ? 16 : 28);  // every warp of the groups
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(bar(C::kScoresDone + i), 1);
             tc::mbar_init(bar(C::kProbsReady + i), 8);
-            tc::mbar_init(bar(C::kOutDone + i), 1);
-            tc::mbar_init(bar(C::kOutFree + i), 4);
             tc::mbar_init(bar(C::kWeightsReady + i), 8);
             tc::mbar_init(bar(C::kWeightsFree + i), 1);
+            tc::mbar_init(bar(C::kDeltaDone + i), 1);
+            tc::mbar_init(bar(C::kDeltaFree + i), 8);
         }
-        tc::mbar_init(bar(C::kDeltaDone), 1);
-        tc::mbar_init(bar(C::kDeltaFree), 8);
+        tc::mbar_init(bar(C::kOutDone), 1);
+        tc::mbar_init(bar(C::kOutFree), 4);
         tc::mbar_init(bar(C::kStateReady), 8);
         tc::mbar_init(bar(C::kInterDone), 1);
         tc::mbar_init(bar(C::kInterFree), 4);
@@ -179,7 +186,7 @@ __global__ void __launch_bounds__(kLcThreads, 1)
     bool good = true;
     // a warp of a group: waits together
     auto wait = [&](int which, uint32_t parity) {
-        good = __all_sync(0xffffffffu, tc::mbar_wait(bar(which), parity));
+        good = tc::mbar_wait_warp(bar(which), parity);
         tc::fence_after();
         return good;
     };
@@ -187,44 +194,51 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         if (lane == 0)
             tc::mbar_arrive(bar(which));
     };
-    // one thread
-    auto ready = [&](int which, uint32_t parity) {
-        good = good && tc::mbar_wait(bar(which), parity);
-        tc::fence_after();
-        return good;
-    };
+    auto decay_slot = [&](int c) { return c % C::kDecays; };
+    auto decays_ready = [&](int c) { return wait(C::kDecFull + decay_slot(c), (c / C::kDecays) & 1); };
     const int quarter = warp % 4;                // of the 128 lanes of tensor memory
     const uint32_t lanes = tmem + ((uint32_t)quarter << 21);
     const int row = quarter * 32 + lane;
 
     if (warp == 0) {
         if (lane == 0) {
-            int issued = 0;
-            for (int c = 0; c < chunks; ++c, ++issued) {
-                const uint32_t i = c % C::kSlots, round = (c / C::kSlots) & 1;
-                const int t0 = t_first + c * kLcChunk;
-                if (!ready(C::kKFree + i, round ^ 1u) || (!STATES && !ready(C::kQFree + i, round ^ 1u)))
-                    break;
-                tc::mbar_expect(bar(C::kQkFull + i), (STATES ? 1 : 2) * C::kQK);
+            // A slot of V is free again when its P V is done, one of K after the state's product, one of Q after Q S:
+            // whichever is free next is filled next.
+            const CUtensorMap *const maps[3] = {&map_k, &map_v, &map_q};
+            int next[3] = {0, 0, STATES ? chunks : 0};
+            for (int polls = 0; min(min(next[0], next[1]), next[2]) < chunks;) {
+                bool idle = true;
 #pragma unroll
-                for (int x = 0; x < DK / 64; ++x) {
-                    const uint32_t at = i * C::kQK + x * kLcBlock;
-                    tc::tma_load_4d(base + C::kKAt + at, &map_k, bar(C::kQkFull + i), 64 * x, group, t0, b);
-                    if (!STATES)
-                        tc::tma_load_4d(base + C::kQAt + at, &map_q, bar(C::kQkFull + i), 64 * x, group, t0, b);
+                for (int x = 0; x < 3; ++x) {
+                    const int c = next[x], i = c % C::kSlots;
+                    const int free = x == 0 ? C::kKFree : x == 1 ? C::kVFree : C::kQFree;
+                    const int full = x == 0 ? C::kKFull : x == 1 ? C::kVFull : C::kQFull;
+                    if (c >= chunks || !tc::mbar_test(bar(free + i), ((c / C::kSlots) & 1) ^ 1u))
+                        continue;
+                    const uint32_t bytes = x == 1 ? kLcBlock : C::kQK;
+                    const uint32_t at = base + (x == 0 ? C::kKAt : x == 1 ? C::kVAt : C::kQAt) + i * bytes;
+                    tc::mbar_expect(bar(full + i), bytes);
+#pragma unroll
+                    for (int y = 0; y < (x == 1 ? 1 : DK / 64); ++y)
+                        tc::tma_load_4d(at + y * kLcBlock, maps[x], bar(full + i), (x == 1 ? c0 : 0) + 64 * y,
+                                        x == 1 ? h : group, t_first + c * kLcChunk, b);
+                    next[x] = c + 1;
+                    idle = false;
                 }
-                if (!ready(C::kVFree + i, round ^ 1u)) {
-                    tc::mbar_wait(bar(C::kQkFull + i), round);
+                polls = idle ? polls + 1 : 0;
+                if (polls > kLcIdlePolls) {
+                    good = false;
                     break;
                 }
-                tc::mbar_expect(bar(C::kVFull + i), kLcBlock);
-                tc::tma_load_4d(base + C::kVAt + i * kLcBlock, &map_v, bar(C::kVFull + i), c0, h, t0, b);
+                if (idle)
+                    __nanosleep(20);
             }
             // copies must have landed before the CTA's shared memory goes
-            for (int c = max(0, issued - C::kSlots); c < issued; ++c) {
-                tc::mbar_wait(bar(C::kQkFull + c % C::kSlots), (c / C::kSlots) & 1);
-                tc::mbar_wait(bar(C::kVFull + c % C::kSlots), (c / C::kSlots) & 1);
-            }
+#pragma unroll
+            for (int x = 0; x < (STATES ? 2 : 3); ++x)
+                for (int c = max(0, next[x] - C::kSlots); c < next[x]; ++c)
+                    tc::mbar_wait(bar((x == 0 ? C::kKFull : x == 1 ? C::kVFull : C::kQFull) + c % C::kSlots),
+                                  (c / C::kSlots) & 1);
         }
     } else if (warp == 1 && !STATES) {
         // descriptors of the first slot's tiles; an address enters them in units of 16 bytes
@@ -234,7 +248,7 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         auto scores = [&](int c) {
             // the buffer is free: the P V of two chunks before, which reads P in its place, was issued before
             const uint32_t i = c % C::kSlots;
-            if (!wait(C::kQkFull + i, (c / C::kSlots) & 1))
+            if (!wait(C::kKFull + i, (c / C::kSlots) & 1) || !wait(C::kQFull + i, (c / C::kSlots) & 1))
                 return;
             const uint64_t q = q_k + i * (C::kQK / 16), k = k_k + i * (C::kQK / 16);
             if (tc::elect_one()) {
@@ -253,23 +267,28 @@ __global__ void __launch_bounds__(kLcThreads, 1)
             scores(0);
         for (int c = 0; c < chunks && good; ++c) {
             const uint32_t i = c % C::kSlots, round = (c / C::kSlots) & 1, two = c & 1, turn = (c >> 1) & 1;
-            if (c + 1 < chunks)
+            // the next chunk's scores first, unless its tiles are still on their way
+            const bool ahead = c + 1 < chunks && tc::mbar_test_warp(bar(C::kKFull + (c + 1) % C::kSlots), ((c + 1) / C::kSlots) & 1) &&
+                               tc::mbar_test_warp(bar(C::kQFull + (c + 1) % C::kSlots), ((c + 1) / C::kSlots) & 1);
+            if (ahead)
                 scores(c + 1);
             // P V; P of 16 tokens lies in the first 8 of their 16 columns of the scores.  In a chunk that is not
             // full the weight warps clear the rows of V behind the last token.
-            if (!wait(C::kVFull + i, round) || !wait(C::kProbsReady + two, turn) || !wait(C::kOutFree + two, turn ^ 1u) ||
+            if (!wait(C::kVFull + i, round) || !wait(C::kProbsReady + two, turn) || !wait(C::kOutFree, two ^ 1u) ||
                 (t_first + (c + 1) * kLcChunk > t_end && !wait(C::kWeightsReady, two)))
                 break;
             const uint64_t v = v_mn + i * (kLcBlock / 16);
             if (tc::elect_one()) {
 #pragma unroll
                 for (int j = 0; j < kLcChunk / 16; ++j)
-                    tc::mma_bf16_ta(tmem + kLcOutAt + two * kLcCols, tmem + kLcScoresAt + two * 128 + j * 16,
+                    tc::mma_bf16_ta(tmem + kLcOutAt, tmem + kLcScoresAt + two * 128 + j * 16,
                                     v + j * (2048 / 16), lc_idesc(kLcCols, false, true), j > 0);
-                tc::commit(bar(C::kOutDone + two));
+                tc::commit(bar(C::kOutDone));
                 tc::commit(bar(C::kVFree + i));
             }
             __syncwarp();
+            if (!ahead && c + 1 < chunks)
+                scores(c + 1);
         }
     } else if (warp == 3) {
         const uint64_t q_k = tc::swizzled_desc(base + C::kQAt, 16, 1024);         // K-major
@@ -279,9 +298,10 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         constexpr uint32_t kStep = 2048 / 16;  // 16 tokens (or rows of S) of an MN-major tile
         for (int c = 0; c < chunks && good; ++c) {
             const uint32_t i = c % C::kSlots, turn = c & 1;
+            const uint32_t two = c & 1;  // of the buffers of K^T (w V)
             // K^T (w V): lanes are rows of S.  With DK = 64 the upper 64 lanes read what lies behind the tile and
             // give rows that nobody reads.
-            if (!wait(C::kQkFull + i, (c / C::kSlots) & 1) || !wait(C::kDeltaFree, turn ^ 1u))
+            if (!wait(C::kKFull + i, (c / C::kSlots) & 1) || !wait(C::kDeltaFree + two, ((c >> 1) & 1) ^ 1u))
                 break;
             const uint64_t kt = k_mn + i * (C::kQK / 16);
             for (int half = 0; half < 2 && wait(C::kWeightsReady + half, turn); ++half) {
@@ -290,12 +310,12 @@ __global__ void __launch_bounds__(kLcThreads, 1)
                     for (int part = 0; part < kLcParts; ++part)
 #pragma unroll
                         for (int j = 0; j < kLcChunk / 32; ++j)
-                            tc::mma_bf16(tmem + kLcDeltaAt, kt + (half * 4 + j) * kStep,
+                            tc::mma_bf16(tmem + kLcDeltaAt + two * kLcCols, kt + (half * 4 + j) * kStep,
                                          w_mn + part * (kLcBlock / 16) + (half * 4 + j) * kStep,
                                          lc_idesc(kLcCols, true, true), half > 0 || part > 0 || j > 0);
                     tc::commit(bar(C::kWeightsFree + half));
                     if (half) {
-                        tc::commit(bar(C::kDeltaDone));
+                        tc::commit(bar(C::kDeltaDone + two));
                         tc::commit(bar(C::kKFree + i));
                     }
                 }
@@ -306,7 +326,7 @@ __global__ void __launch_bounds__(kLcThreads, 1)
             if (STATES)
                 continue;
             // Q S
-            if (!wait(C::kStateReady, turn) || !wait(C::kInterFree, turn ^ 1u))
+            if (!wait(C::kQFull + i, (c / C::kSlots) & 1) || !wait(C::kStateReady, turn) || !wait(C::kInterFree, turn ^ 1u))
                 break;
             const uint64_t q = q_k + i * (C::kQK / 16);
             if (tc::elect_one()) {
@@ -323,63 +343,78 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         // Four tokens of each lane, eight lanes of each block.
         const float fixed = a.per_token ? 0.0f : a.log_decay[h];
         const float *gates = a.log_decay + (a.per_token ? ((long long)b * a.L) * a.H + h : 0);
-        float g[4];
+        float g[4];  // of the next chunk, on their way while this one's are summed
         auto fetch = [&](int c) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int t = t_first + c * kLcChunk + lane * 4 + j;
-                g[j] = t >= t_end ? 0.0f : la_clamp(a.per_token ? gates[(long long)t * a.H] : fixed);
+                g[j] = t >= t_end ? 0.0f : a.per_token ? gates[(long long)t * a.H] : fixed;
             }
         };
         double whole = 0.0;
         if (chunks > 0)
             fetch(0);
         for (int c = 0; c < chunks; ++c) {
-            const uint32_t i = c % C::kSlots, round = (c / C::kSlots) & 1;
-            double s[4];
+            // cb_j, the sum from a block's end back to j, added from the end: where a weight exp(-cb) counts, cb is
+            // small, and so is its rounding.  The same for the blocks within the chunk.
+            float after[4];  // of the lane's tokens: the lane's later ones
+            after[3] = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                s[j] = (j ? s[j - 1] : 0.0) + (double)g[j] * 1.4426950408889634;
+            for (int j = 2; j >= 0; --j)
+                after[j] = after[j + 1] + la_clamp(g[j + 1]) * kLcLog2e;
+            const float own = after[0] + la_clamp(g[0]) * kLcLog2e;
             if (c + 1 < chunks)
                 fetch(c + 1);
-            double before = s[3];
+            float sum = own;  // of this lane and the block's later ones
 #pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                const double v = __shfl_up_sync(0xffffffffu, before, d);
-                if (lane >= d)
-                    before += v;
+            for (int d = 1; d < 8; d *= 2) {
+                const float v = __shfl_down_sync(0xffffffffu, sum, d, 8);
+                if (lane % 8 + d < 8)
+                    sum += v;
             }
-            const double end = before;
-            before = __shfl_up_sync(0xffffffffu, before, 1);
-            if (lane == 0)
-                before = 0.0;
-            double m[4];
+            float later = __shfl_down_sync(0xffffffffu, sum, 1, 8);
+            if (lane % 8 == 7)
+                later = 0.0f;
+            float blocks[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                m[q] = __shfl_sync(0xffffffffu, end, 8 * q + 7);
-            if (!wait(C::kDecFree + i, round ^ 1u))
+                blocks[q] = __shfl_sync(0xffffffffu, sum, 8 * q);
+            if (!wait(C::kDecFree + decay_slot(c), (c / C::kDecays & 1) ^ 1u))
                 break;
-            ChunkDecay &out = decay[i];
-            const double mine = lane < 8 ? m[0] : lane < 16 ? m[1] : lane < 24 ? m[2] : m[3];
+            ChunkDecay &out = decay[decay_slot(c)];
+            float cb[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float cb = (float)((j < 3 ? before + s[j] : end) - mine);
-                out.cb[lane * 4 + j] = cb;
-                out.f[lane * 4 + j] = exp2f(-cb);
-            }
+            for (int j = 0; j < 4; ++j)
+                cb[j] = -(later + after[j]);
+            *reinterpret_cast<float4 *>(&out.cb[lane * 4]) = make_float4(cb[0], cb[1], cb[2], cb[3]);
+            *reinterpret_cast<float4 *>(&out.f[lane * 4]) =
+                make_float4(exp2f(-cb[0]), exp2f(-cb[1]), exp2f(-cb[2]), exp2f(-cb[3]));
+            const float all = ((blocks[3] + blocks[2]) + blocks[1]) + blocks[0];
             if (lane < 4) {
-                const double own = lane == 0 ? m[0] : lane == 1 ? m[1] : lane == 2 ? m[2] : m[3];
-                out.m[lane] = (float)own;
-                out.e[lane] = exp2f((float)(m[3] - own));
+                float to_end = 0.0f, to_here = 0.0f;
+#pragma unroll
+                for (int q = 3; q >= 0; --q)
+                    to_end += q > lane ? blocks[q] : 0.0f;
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    out.dm[q][lane] = (float)(m[q] - own);
-                if (lane == 0)
-                    out.total = exp2f((float)m[3]);
+                    to_here += q <= lane ? blocks[q] : 0.0f;
+                out.m[lane] = to_here;
+                out.e[lane] = exp2f(to_end);
+                float between = 0.0f;  // of blocks lane + 1 .. q
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    between += q > lane ? blocks[q] : 0.0f;
+                    out.dm[q][lane] = between;
+                }
+                if (lane == 0) {
+                    const bool slow = all > -0.5f;
+                    out.keep = slow ? 1.0f : 0.0f;
+                    out.grow = slow ? expm1f(all * kLcLn2) : exp2f(all);
+                }
             }
-            whole += m[3];
+            whole += all;
             __syncwarp();
-            arrive(C::kDecFull + i);
+            arrive(C::kDecFull + decay_slot(c));
         }
         if (STATES && lane == 0 && good)
             p.decays[bh * p.nseg + seg] = exp2f((float)whole);
@@ -390,10 +425,10 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         for (int c = 0; c < chunks && good; ++c) {
             const uint32_t i = c % C::kSlots, round = (c / C::kSlots) & 1, turn = c & 1;
             const int n = min(kLcChunk, t_end - t_first - c * kLcChunk);
-            const ChunkDecay &d = decay[i];
+            const ChunkDecay &d = decay[decay_slot(c)];
             unsigned char *const tileV = smem + C::kVAt + i * kLcBlock;
             unsigned char *const tileW = smem + C::kWAt;
-            if (!wait(C::kDecFull + i, round) || !wait(C::kVFull + i, round) || (n < kLcChunk && !wait(C::kQkFull + i, round)))
+            if (!decays_ready(c) || !wait(C::kVFull + i, round) || (n < kLcChunk && !wait(C::kKFull + i, round)))
                 break;
             for (int half = 0; half < 2; ++half) {
                 uint4 v[2];
@@ -445,68 +480,71 @@ __global__ void __launch_bounds__(kLcThreads, 1)
                 arrive(C::kWeightsReady + half);
             }
             arrive(C::kVFree + i);
-            arrive(C::kDecFree + i);
+            arrive(C::kDecFree + decay_slot(c));
         }
     } else if (warp >= kLcScore && warp < kLcState && !STATES) {
         const int half = (warp - kLcScore) / 4;  // 16 of a block's 32 columns
         for (int c = 0; c < chunks; ++c) {
             const uint32_t i = c % C::kSlots, round = (c / C::kSlots) & 1;
             const uint32_t two = c & 1, turn2 = (c >> 1) & 1;  // of the scores' two buffers
-            const ChunkDecay &d = decay[i];
-            if (!wait(C::kDecFull + i, round) || !wait(C::kScoresDone + two, turn2))
+            const ChunkDecay &d = decay[decay_slot(c)];
+            if (!decays_ready(c) || !wait(C::kScoresDone + two, turn2))
                 break;
             const float cb = d.cb[row];
-            const float2 scale2 = make_float2(a.scale, a.scale), cb2 = make_float2(cb, cb);
+            const uint32_t at = lanes + kLcScoresAt + two * 128 + half * 16;
+            auto factors = [&](const float *from, float2 (&f)[8]) {
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const float4 v = reinterpret_cast<const float4 *>(from + half * 16)[y];
+                    f[2 * y] = make_float2(v.x, v.y), f[2 * y + 1] = make_float2(v.z, v.w);
+                }
+            };
+            auto probs = [&](uint32_t (&v)[16], const float2 (&f)[8], uint32_t (&w)[8]) {
+                tc::tmem_wait16(v);
+#pragma unroll
+                for (int y = 0; y < 8; ++y) {
+                    const float2 r = __fmul2_rn(f[y], make_float2(__uint_as_float(v[2 * y]), __uint_as_float(v[2 * y + 1])));
+                    w[y] = lc_pack(r.x, r.y);
+                }
+            };
+            uint32_t v[16], w[8];
+            float2 f[8];
 #pragma unroll 1
-            for (int blk = 0; blk < 4; ++blk) {
-                const uint32_t at = lanes + kLcScoresAt + two * 128 + blk * 32 + half * 16;
-                uint32_t w[8];
+            for (int blk = 0; blk < quarter; ++blk) {
+                tc::tmem_ld16(at + blk * 32, v);
+                const float r = a.scale * lc_ex2(cb + d.dm[quarter][blk]);
+                factors(d.f + blk * 32, f);
 #pragma unroll
                 for (int y = 0; y < 8; ++y)
-                    w[y] = 0;
-                if (blk <= quarter) {
-                    uint32_t v[16];
-                    tc::tmem_ld16(at, v);
-                    const float4 *const f4 = reinterpret_cast<const float4 *>((blk < quarter ? d.f : d.cb) + blk * 32 + half * 16);
-                    float2 f[8];
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const float4 f_ = f4[y];
-                        f[2 * y] = make_float2(f_.x, f_.y), f[2 * y + 1] = make_float2(f_.z, f_.w);
-                    }
-                    if (blk < quarter) {
-                        const float r = a.scale * lc_ex2(cb + d.dm[quarter][blk]);
-#pragma unroll
-                        for (int y = 0; y < 8; ++y)
-                            f[y] = __fmul2_rn(f[y], make_float2(r, r));
-                    } else {
-#pragma unroll
-                        for (int y = 0; y < 8; ++y) {
-                            const float2 e = __fadd2_rn(cb2, make_float2(-f[y].x, -f[y].y));
-                            f[y] = __fmul2_rn(scale2, make_float2(lc_ex2(e.x), lc_ex2(e.y)));
-                        }
-                    }
-                    tc::tmem_wait16(v);
-#pragma unroll
-                    for (int y = 0; y < 8; ++y) {
-                        const float2 r = __fmul2_rn(f[y], make_float2(__uint_as_float(v[2 * y]), __uint_as_float(v[2 * y + 1])));
-                        w[y] = lc_pack(r.x, r.y);
-                    }
-                    if (blk == quarter) {
-                        // columns behind the row's own token: none
-                        const int last = lane - half * 16;
-#pragma unroll
-                        for (int y = 0; y < 8; ++y)
-                            w[y] &= (2 * y <= last ? 0xffffu : 0u) | (2 * y + 1 <= last ? 0xffff0000u : 0u);
-                    }
-                }
-                tc::tmem_st8(at, w);
+                    f[y] = __fmul2_rn(f[y], make_float2(r, r));
+                probs(v, f, w);
+                tc::tmem_st8(at + blk * 32, w);
             }
+            tc::tmem_ld16(at + quarter * 32, v);
+            factors(d.cb + quarter * 32, f);
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+                const float2 e = __fadd2_rn(make_float2(cb, cb), make_float2(-f[y].x, -f[y].y));
+                f[y] = __fmul2_rn(make_float2(a.scale, a.scale), make_float2(lc_ex2(e.x), lc_ex2(e.y)));
+            }
+            probs(v, f, w);
+            // columns behind the row's own token: none
+            const int last = lane - half * 16;
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+                w[y] &= (2 * y <= last ? 0xffffu : 0u) | (2 * y + 1 <= last ? 0xffff0000u : 0u);
+            tc::tmem_st8(at + quarter * 32, w);
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+                w[y] = 0;
+#pragma unroll 1
+            for (int blk = quarter + 1; blk < 4; ++blk)
+                tc::tmem_st8(at + blk * 32, w);
             tc::tmem_wait_st();
             tc::fence_before();
             __syncwarp();
             arrive(C::kProbsReady + two);
-            arrive(C::kDecFree + i);
+            arrive(C::kDecFree + decay_slot(c));
         }
     } else if (warp >= kLcState && warp < kLcOutput) {
         const int half = (warp - kLcState) / 4;  // of the columns
@@ -542,27 +580,29 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         if (!STATES)
             publish();
         for (int c = 0; c < chunks; ++c) {
-            const uint32_t i = c % C::kSlots, round = (c / C::kSlots) & 1, turn = c & 1;
-            if (!wait(C::kDecFull + i, round))
+            const uint32_t turn = c & 1;
+            if (!decays_ready(c))
                 break;
-            const float2 total = make_float2(decay[i].total, decay[i].total);
+            const float2 grow = make_float2(decay[decay_slot(c)].grow, decay[decay_slot(c)].grow);
+            const float2 keep = make_float2(decay[decay_slot(c)].keep, decay[decay_slot(c)].keep);
             __syncwarp();
-            arrive(C::kDecFree + i);
-            if (!wait(C::kDeltaDone, turn))
+            arrive(C::kDecFree + decay_slot(c));
+            if (!wait(C::kDeltaDone + turn, (c >> 1) & 1))
                 break;
 #pragma unroll
             for (int x = 0; x < kMine / 16; ++x) {
                 uint32_t v[16];
-                tc::tmem_ld16(lanes + kLcDeltaAt + half * kMine + 16 * x, v);
+                tc::tmem_ld16(lanes + kLcDeltaAt + turn * kLcCols + half * kMine + 16 * x, v);
                 tc::tmem_wait16(v);
 #pragma unroll
                 for (int y = 0; y < 8; ++y)
-                    s[8 * x + y] = __ffma2_rn(s[8 * x + y], total,
-                                              make_float2(__uint_as_float(v[2 * y]), __uint_as_float(v[2 * y + 1])));
+                    s[8 * x + y] = __ffma2_rn(s[8 * x + y], keep,
+                                              __ffma2_rn(s[8 * x + y], grow, make_float2(__uint_as_float(v[2 * y]),
+                                                                                         __uint_as_float(v[2 * y + 1]))));
             }
             tc::fence_before();
             __syncwarp();
-            arrive(C::kDeltaFree);
+            arrive(C::kDeltaFree + turn);
             if (!STATES) {
                 // Q S has read the copy that is replaced now
                 if (!wait(C::kInterDone, turn))
@@ -581,21 +621,21 @@ __global__ void __launch_bounds__(kLcThreads, 1)
     } else if (warp >= kLcOutput && !STATES) {
         const bool wide = a.Dv % 16 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
         for (int c = 0; c < chunks; ++c) {
-            const uint32_t i = c % C::kSlots, round = (c / C::kSlots) & 1, turn = c & 1;
+            const uint32_t turn = c & 1;
             const int t = t_first + c * kLcChunk + row;
-            if (!wait(C::kDecFull + i, round))
+            if (!decays_ready(c))
                 break;
-            const float r = a.scale * lc_ex2(decay[i].cb[row] + decay[i].m[quarter]);
+            const float r = a.scale * lc_ex2(decay[decay_slot(c)].cb[row] + decay[decay_slot(c)].m[quarter]);
             __syncwarp();
-            arrive(C::kDecFree + i);
-            if (!wait(C::kInterDone, turn) || !wait(C::kOutDone + (c & 1), (c >> 1) & 1))
+            arrive(C::kDecFree + decay_slot(c));
+            if (!wait(C::kInterDone, turn) || !wait(C::kOutDone, turn))
                 break;
             __nv_bfloat16 *const o = a.out + (((long long)b * a.L + t) * a.H + h) * a.Dv + c0;
 #pragma unroll 1
             for (int x = 0; x < kLcCols / 16; ++x) {
                 uint32_t u[16], v[16], w[8];
                 tc::tmem_ld16(lanes + kLcInterAt + 16 * x, u);
-                tc::tmem_ld16(lanes + kLcOutAt + (c & 1) * kLcCols + 16 * x, v);
+                tc::tmem_ld16(lanes + kLcOutAt + 16 * x, v);
                 tc::tmem_wait16(u);
                 tc::tmem_wait16(v);
 #pragma unroll
@@ -617,7 +657,7 @@ __global__ void __launch_bounds__(kLcThreads, 1)
             tc::fence_before();
             __syncwarp();
             arrive(C::kInterFree);
-            arrive(C::kOutFree + (c & 1));
+            arrive(C::kOutFree);
         }
     }
     if (!good && lane == 0)

@@ -45,6 +45,44 @@ __device__ __forceinline__ bool elect_one()
     return one != 0;
 }
 
+// mbar_wait for a warp that waits together (all lanes poll, all lanes agree on the result), with the bound
+// of tcgen05.cuh.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t mbar, uint32_t phase)
+{
+    uint32_t done;
+    int left = (int)kSpinLimit;
+    do {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(done)
+            : "r"(mbar), "r"(phase)
+            : "memory");
+    } while (!__all_sync(0xffffffffu, done) && --left);
+    return left != 0;
+}
+
+// Whether the phase has completed.
+__device__ __forceinline__ bool mbar_test(uint32_t mbar, uint32_t phase)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(mbar), "r"(phase)
+        : "memory");
+    return done != 0;
+}
+
+// The same answer for the whole warp.
+__device__ __forceinline__ bool mbar_test_warp(uint32_t mbar, uint32_t phase)
+{
+    return __all_sync(0xffffffffu, mbar_test(mbar, phase));
+}
+
 __device__ __forceinline__ void mbar_init(uint32_t mbar, uint32_t count)
 {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(mbar), "r"(count) : "memory");
