@@ -8,6 +8,7 @@ device's current stream.  Outputs and workspaces allocated here belong to that s
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -15,6 +16,7 @@ from ._binding import SS2D_BF16, SS2D_F32, Ss2dError, _check, load_library
 
 SS2D_E4M3 = 2
 FP8_BLOCK = 128
+_NO_SIZE = ctypes.c_size_t(-1).value
 _OUT_CODE = {torch.float32: SS2D_F32, torch.bfloat16: SS2D_BF16, torch.float8_e4m3fn: SS2D_E4M3}
 
 
@@ -65,6 +67,9 @@ class LinearAttentionStepArgs(ctypes.Structure):
     ]
 
 
+_MATMUL_SIZE = ctypes.sizeof(MatmulFp8Args)
+_ATTENTION_SIZE = ctypes.sizeof(LinearAttentionArgs)
+_STEP_SIZE = ctypes.sizeof(LinearAttentionStepArgs)
 _lib = None
 
 
@@ -95,22 +100,25 @@ class _Call:
     """The device and stream of one call: `with _Call(x, stream) as c` makes the device current
     and c.new(...) allocates on the call's stream."""
 
-    __slots__ = ("device", "stream", "_guard", "_foreign")
+    __slots__ = ("index", "device", "handle", "_stream", "_guard")
 
     def __init__(self, t, stream):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise ValueError("libss2d takes device tensors")
         self.device = t.device
-        current = torch.cuda.current_stream(t.device)
-        if stream is not None and stream.device != t.device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
-        self._foreign = current if stream is not None and stream.cuda_stream != current.cuda_stream else None
-        self.stream = current if stream is None else stream
-        self._guard = None
+        self.index = t.get_device()
+        self.handle = torch._C._cuda_getCurrentRawStream(self.index)
+        self._stream = self._guard = None
+        if stream is not None:
+            if stream.device != self.device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {self.device}")
+            if stream.cuda_stream != self.handle:
+                self.handle = stream.cuda_stream
+                self._stream = stream
 
     def __enter__(self):
-        if self.device.index != torch.cuda.current_device():
-            self._guard = torch.cuda.device(self.device)
+        if self.index != torch._C._cuda_getDevice():
+            self._guard = torch.cuda.device(self.index)
             self._guard.__enter__()
         return self
 
@@ -119,54 +127,58 @@ class _Call:
             self._guard.__exit__(*exc)
 
     def new(self, shape, dtype):
-        if self._foreign is None:
+        if self._stream is None:
             return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(self.stream):
+        with torch.cuda.stream(self._stream):
             t = torch.empty(shape, dtype=dtype, device=self.device)
-        t.record_stream(self._foreign)
+        t.record_stream(torch.cuda.current_stream(self.index))
         return t
+
+    def like(self, t, dtype):
+        """new(t.shape, dtype) of a dense t."""
+        return torch.empty_like(t, dtype=dtype) if self._stream is None else self.new(t.shape, dtype)
 
     def ptr(self, t, name, dtype, shape):
         """The pointer of a dense tensor of this device, type and shape; None stays None."""
         if t is None:
             return None
-        self.check(t, name, dtype, shape)
+        if t.get_device() != self.index or t.dtype != dtype or t.shape != shape:
+            self._refuse(t, name, dtype, shape)
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
         return t.data_ptr()
 
-    def check(self, t, name, dtype, shape):
-        if t.device != self.device:
+    def strided(self, t, name, shape):
+        """Pointer and strides of a bf16 tensor with a dense last dimension."""
+        if t.get_device() != self.index or t.dtype != torch.bfloat16 or t.shape != shape:
+            self._refuse(t, name, torch.bfloat16, shape)
+        strides = t.stride()
+        if strides[-1] != 1 and shape[-1] > 1:
+            raise ValueError(f"the last dimension of {name} must be dense")
+        return t.data_ptr(), strides
+
+    def _refuse(self, t, name, dtype, shape):
+        if t.get_device() != self.index:
             raise ValueError(f"{name} is on {t.device}, not on {self.device}")
         if t.dtype != dtype:
             raise ValueError(f"{name} must be {str(dtype).removeprefix('torch.')}")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-
-    def strided(self, t, name, shape):
-        """Pointer and leading strides of a bf16 tensor with a dense last dimension."""
-        self.check(t, name, torch.bfloat16, shape)
-        if t.stride(-1) != 1 and t.shape[-1] > 1:
-            raise ValueError(f"the last dimension of {name} must be dense")
-        return t.data_ptr(), t.stride()[:-1]
-
-    @property
-    def handle(self):
-        return self.stream.cuda_stream
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
 def _float_code(t, name):
-    if t.dtype not in (torch.float32, torch.bfloat16):
+    code = _OUT_CODE.get(t.dtype)
+    if code is None or code == SS2D_E4M3:
         raise ValueError(f"{name} must be float32 or bfloat16")
-    return _OUT_CODE[t.dtype]
+    return code
 
 
 def _workspace(call, workspace, need):
-    if need == ctypes.c_size_t(-1).value:
+    if not need:
         return None, 0, None  # the call itself says what is wrong with its arguments
     if workspace is None:
         workspace = call.new((need,), torch.uint8)
-    elif workspace.device != call.device or not workspace.is_contiguous():
+        return workspace.data_ptr(), need, workspace
+    if workspace.get_device() != call.index or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {call.device}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
@@ -182,66 +194,51 @@ def rms_norm(x, weight, residual=None, eps=1e-6, out_dtype=torch.bfloat16, y=Non
     allocated here; a given y keeps its own.  scales (..., ceil(D / 128)) fp32 holds one scale
     for each 128 columns of a row.  residual_out may be `residual` itself.
     """
-    if out_dtype not in _OUT_CODE:
-        raise ValueError("out_dtype must be float32, bfloat16 or float8_e4m3fn")
     with _Call(x, stream) as c:
-        if x.dim() == 0:
+        shape = x.shape
+        if not shape:
             raise ValueError("x must have a last dimension")
-        D = x.shape[-1]
+        D = shape[-1]
         rows = x.numel() // D if D else 0
-        xp = c.ptr(x, "x", x.dtype, x.shape)
         xc = _float_code(x, "x")
+        xp = c.ptr(x, "x", x.dtype, shape)
         wp = c.ptr(weight, "weight", torch.float32, (D,))
         rp, rc, rop = None, 0, None
         if residual is not None:
             rc = _float_code(residual, "residual")
-            rp = c.ptr(residual, "residual", residual.dtype, x.shape)
+            rp = c.ptr(residual, "residual", residual.dtype, shape)
             if residual_out is None:
-                residual_out = c.new(x.shape, residual.dtype)
-            rop = c.ptr(residual_out, "residual_out", residual.dtype, x.shape)
+                residual_out = c.like(residual, residual.dtype)
+                rop = residual_out.data_ptr()
+            else:
+                rop = c.ptr(residual_out, "residual_out", residual.dtype, shape)
         elif residual_out is not None:
             raise ValueError("residual_out is given without a residual")
         if y is None:
-            y = c.new(x.shape, out_dtype)
-        elif y.dtype not in _OUT_CODE:
-            raise ValueError("y must be float32, bfloat16 or float8_e4m3fn")
-        yp = c.ptr(y, "y", y.dtype, x.shape)
+            code = _OUT_CODE.get(out_dtype)
+            if code is None:
+                raise ValueError("out_dtype must be float32, bfloat16 or float8_e4m3fn")
+            y = c.like(x, out_dtype)
+            yp = y.data_ptr()
+        else:
+            code = _OUT_CODE.get(y.dtype)
+            if code is None:
+                raise ValueError("y must be float32, bfloat16 or float8_e4m3fn")
+            yp = c.ptr(y, "y", y.dtype, shape)
         sp = None
-        if y.dtype == torch.float8_e4m3fn:
-            shape = x.shape[:-1] + (-(-D // FP8_BLOCK),)
+        if code == SS2D_E4M3:
+            groups = shape[:-1] + (-(-D // FP8_BLOCK),)
             if scales is None:
-                scales = c.new(shape, torch.float32)
-            sp = c.ptr(scales, "scales", torch.float32, shape)
+                scales = c.new(groups, torch.float32)
+            sp = c.ptr(scales, "scales", torch.float32, groups)
         elif scales is not None:
             raise ValueError("scales is given without a float8_e4m3fn y")
-        _check(_library().ss2d_rms_norm(xp, xc, rp, rc, wp, eps, yp, _OUT_CODE[y.dtype], sp, rop, rows, D, c.handle),
-               "ss2d_rms_norm")
-    got = (y,)
-    if scales is not None:
-        got += (scales,)
-    if residual is not None:
-        got += (residual_out,)
-    return got if len(got) > 1 else y
-
-
-def _matmul_args(c, a, a_scales, w, w_scales, bias, out_dtype):
-    if a.dim() < 1 or w.dim() != 2:
-        raise ValueError("a must be (..., K) and w (N, K)")
-    K, N = a.shape[-1], w.shape[0]
-    M = a.numel() // K if K else 0
-    if max(M, N, K) > 0x7fffffff:
-        raise ValueError("sizes must fit 32 bits")
-    kb, nb = -(-K // FP8_BLOCK), -(-N // FP8_BLOCK)
-    args = MatmulFp8Args()
-    args.struct_size = ctypes.sizeof(MatmulFp8Args)
-    args.M, args.N, args.K = M, N, K
-    args.a = c.ptr(a, "a", torch.float8_e4m3fn, a.shape)
-    args.a_scales = c.ptr(a_scales, "a_scales", torch.float32, a.shape[:-1] + (kb,))
-    args.w = c.ptr(w, "w", torch.float8_e4m3fn, (N, K))
-    args.w_scales = c.ptr(w_scales, "w_scales", torch.float32, (nb, kb))
-    args.bias = c.ptr(bias, "bias", torch.float32, (N,))
-    args.c_dtype = {torch.float32: SS2D_F32, torch.bfloat16: SS2D_BF16}[out_dtype]
-    return args
+        status = _library().ss2d_rms_norm(xp, xc, rp, rc, wp, eps, yp, code, sp, rop, rows, D, c.handle)
+        if status:
+            _check(status, "ss2d_rms_norm")
+    if residual is None:
+        return y if scales is None else (y, scales)
+    return (y, residual_out) if scales is None else (y, scales, residual_out)
 
 
 def matmul_fp8(a, a_scales, w, w_scales, bias=None, out_dtype=torch.bfloat16, out=None, workspace=None, stream=None):
@@ -256,29 +253,48 @@ def matmul_fp8(a, a_scales, w, w_scales, bias=None, out_dtype=torch.bfloat16, ou
     when none is given.
     """
     with _Call(a, stream) as c:
+        if a.dim() < 1 or w.dim() != 2:
+            raise ValueError("a must be (..., K) and w (N, K)")
+        lead, K, N = a.shape[:-1], a.shape[-1], w.shape[0]
+        M = a.numel() // K if K else 0
+        if max(M, N, K) > 0x7fffffff:
+            raise ValueError("sizes must fit 32 bits")
         if out is not None:
             out_dtype = out.dtype
-        if out_dtype not in (torch.float32, torch.bfloat16):
+        code = _OUT_CODE.get(out_dtype)
+        if code is None or code == SS2D_E4M3:
             raise ValueError("out must be float32 or bfloat16")
-        args = _matmul_args(c, a, a_scales, w, w_scales, bias, out_dtype)
-        shape = a.shape[:-1] + (w.shape[0],)
+        kb, nb = -(-K // FP8_BLOCK), -(-N // FP8_BLOCK)
+        ap = c.ptr(a, "a", torch.float8_e4m3fn, a.shape)
+        asp = c.ptr(a_scales, "a_scales", torch.float32, lead + (kb,))
+        wp = c.ptr(w, "w", torch.float8_e4m3fn, (N, K))
+        wsp = c.ptr(w_scales, "w_scales", torch.float32, (nb, kb))
+        bp = c.ptr(bias, "bias", torch.float32, (N,))
         if out is None:
-            out = c.new(shape, out_dtype)
-        args.c = c.ptr(out, "out", out_dtype, shape)
+            out = c.new(lead + (N,), out_dtype)
+        op = c.ptr(out, "out", out_dtype, lead + (N,))
+        args = MatmulFp8Args(_MATMUL_SIZE, M, N, K, ap, asp, wp, wsp, bp, op, code)
         lib = _library()
-        wp, wn, workspace = _workspace(c, workspace, lib.ss2d_matmul_fp8_workspace(args))
-        _check(lib.ss2d_matmul_fp8(args, wp, wn, c.handle), "ss2d_matmul_fp8")
+        sp, sn, workspace = _workspace(c, workspace, _matmul_need(M, N, K))
+        status = lib.ss2d_matmul_fp8(args, sp, sn, c.handle)
+        if status:
+            _check(status, "ss2d_matmul_fp8")
     return out
 
 
-def matmul_fp8_workspace_size(M, N, K, out_dtype=torch.bfloat16) -> int:
+@functools.lru_cache(maxsize=4096)
+def _matmul_need(M, N, K):
+    """Workspace bytes for these sizes, or 0 if they are refused."""
+    n = _library().ss2d_matmul_fp8_workspace(MatmulFp8Args(_MATMUL_SIZE, M, N, K))
+    return 0 if n == _NO_SIZE else n
+
+
+def matmul_fp8_workspace_size(M, N, K) -> int:
     """Workspace bytes ss2d_matmul_fp8 needs for these sizes."""
-    args = MatmulFp8Args(ctypes.sizeof(MatmulFp8Args), M, N, K)
-    args.c_dtype = _OUT_CODE[out_dtype]
-    n = _library().ss2d_matmul_fp8_workspace(args)
-    if n == ctypes.c_size_t(-1).value:
-        raise Ss2dError(1, "SS2D_ERR_INVALID_ARG", _library().ss2d_last_error().decode())
-    return int(n)
+    n = _matmul_need(M, N, K)
+    if not n:
+        raise Ss2dError(1, "SS2D_ERR_INVALID_ARG", f"sizes M={M} N={N} K={K} are refused")
+    return n
 
 
 def _heads(q, k, v, lead):
@@ -305,36 +321,42 @@ def linear_attention(q, k, v, log_decay, scale=1.0, h0=None, lengths=None, retur
     with _Call(q, stream) as c:
         G, H, Dk, Dv = _heads(q, k, v, 2)
         B, L = q.shape[:2]
-        a = LinearAttentionArgs()
-        a.struct_size = ctypes.sizeof(LinearAttentionArgs)
-        a.B, a.L, a.G, a.H, a.Dk, a.Dv = B, L, G, H, Dk, Dv
-        a.q, a.q_stride[:] = c.strided(q, "q", (B, L, G, Dk))
-        a.k, a.k_stride[:] = c.strided(k, "k", (B, L, G, Dk))
-        a.v, a.v_stride[:] = c.strided(v, "v", (B, L, H, Dv))
-        a.decay_per_token = int(log_decay.dim() == 3)
-        a.log_decay = c.ptr(log_decay, "log_decay", torch.float32, (B, L, H) if a.decay_per_token else (H,))
-        a.lengths = c.ptr(lengths, "lengths", torch.int32, (B,))
-        a.scale = scale
-        a.h0 = c.ptr(h0, "h0", torch.float32, (B, H, Dk, Dv))
+        qp, qs = c.strided(q, "q", (B, L, G, Dk))
+        kp, ks = c.strided(k, "k", (B, L, G, Dk))
+        vp, vs = c.strided(v, "v", (B, L, H, Dv))
+        per_token = log_decay.dim() == 3
+        gp = c.ptr(log_decay, "log_decay", torch.float32, (B, L, H) if per_token else (H,))
+        lp = c.ptr(lengths, "lengths", torch.int32, (B,))
+        state = (B, H, Dk, Dv)
+        hp = c.ptr(h0, "h0", torch.float32, state)
         if h_last is None and return_last_state:
-            h_last = c.new((B, H, Dk, Dv), torch.float32)
-        a.h_last = c.ptr(h_last, "h_last", torch.float32, (B, H, Dk, Dv))
+            h_last = c.new(state, torch.float32)
+        hlp = c.ptr(h_last, "h_last", torch.float32, state)
         if out is None:
             out = c.new((B, L, H, Dv), torch.bfloat16)
-        a.out = c.ptr(out, "out", torch.bfloat16, (B, L, H, Dv))
+        op = c.ptr(out, "out", torch.bfloat16, (B, L, H, Dv))
+        a = LinearAttentionArgs(_ATTENTION_SIZE, B, L, G, H, Dk, Dv, qp, kp, vp, qs[:3], ks[:3], vs[:3], gp,
+                                per_token, lp, scale, hp, hlp, op)
         lib = _library()
-        wp, wn, workspace = _workspace(c, workspace, lib.ss2d_linear_attention_workspace(a))
-        _check(lib.ss2d_linear_attention(a, wp, wn, c.handle), "ss2d_linear_attention")
+        wp, wn, workspace = _workspace(c, workspace, _attention_need(B, L, G, H, Dk, Dv))
+        status = lib.ss2d_linear_attention(a, wp, wn, c.handle)
+        if status:
+            _check(status, "ss2d_linear_attention")
     return out if h_last is None else (out, h_last)
+
+
+@functools.lru_cache(maxsize=4096)
+def _attention_need(*sizes):
+    n = _library().ss2d_linear_attention_workspace(LinearAttentionArgs(_ATTENTION_SIZE, *sizes))
+    return 0 if n == _NO_SIZE else n
 
 
 def linear_attention_workspace_size(B, L, G, H, Dk, Dv) -> int:
     """Workspace bytes ss2d_linear_attention needs for these sizes."""
-    a = LinearAttentionArgs(ctypes.sizeof(LinearAttentionArgs), B, L, G, H, Dk, Dv)
-    n = _library().ss2d_linear_attention_workspace(a)
-    if n == ctypes.c_size_t(-1).value:
-        raise Ss2dError(1, "SS2D_ERR_INVALID_ARG", _library().ss2d_last_error().decode())
-    return int(n)
+    n = _attention_need(B, L, G, H, Dk, Dv)
+    if not n:
+        raise Ss2dError(1, "SS2D_ERR_INVALID_ARG", f"sizes B={B} L={L} G={G} H={H} Dk={Dk} Dv={Dv} are refused")
+    return n
 
 
 def linear_attention_step(q, k, v, log_decay, state, slots=None, scale=1.0, out=None, stream=None):
@@ -349,21 +371,21 @@ def linear_attention_step(q, k, v, log_decay, state, slots=None, scale=1.0, out=
     with _Call(q, stream) as c:
         G, H, Dk, Dv = _heads(q, k, v, 1)
         B, pool = q.shape[0], state.shape[0]
-        a = LinearAttentionStepArgs()
-        a.struct_size = ctypes.sizeof(LinearAttentionStepArgs)
-        a.B, a.pool, a.G, a.H, a.Dk, a.Dv = B, pool, G, H, Dk, Dv
-        a.q, a.q_stride[:] = c.strided(q, "q", (B, G, Dk))
-        a.k, a.k_stride[:] = c.strided(k, "k", (B, G, Dk))
-        a.v, a.v_stride[:] = c.strided(v, "v", (B, H, Dv))
-        a.decay_per_token = int(log_decay.dim() == 2)
-        a.log_decay = c.ptr(log_decay, "log_decay", torch.float32, (B, H) if a.decay_per_token else (H,))
-        a.slots = c.ptr(slots, "slots", torch.int32, (B,))
-        a.scale = scale
-        a.state = c.ptr(state, "state", torch.float32, (pool, H, Dk, Dv))
+        qp, qs = c.strided(q, "q", (B, G, Dk))
+        kp, ks = c.strided(k, "k", (B, G, Dk))
+        vp, vs = c.strided(v, "v", (B, H, Dv))
+        per_token = log_decay.dim() == 2
+        gp = c.ptr(log_decay, "log_decay", torch.float32, (B, H) if per_token else (H,))
+        sp = c.ptr(slots, "slots", torch.int32, (B,))
+        hp = c.ptr(state, "state", torch.float32, (pool, H, Dk, Dv))
         if out is None:
             out = c.new((B, H, Dv), torch.bfloat16)
-        a.out = c.ptr(out, "out", torch.bfloat16, (B, H, Dv))
-        _check(_library().ss2d_linear_attention_step(a, c.handle), "ss2d_linear_attention_step")
+        op = c.ptr(out, "out", torch.bfloat16, (B, H, Dv))
+        a = LinearAttentionStepArgs(_STEP_SIZE, B, pool, G, H, Dk, Dv, qp, kp, vp, qs[:2], ks[:2], vs[:2], gp,
+                                    per_token, sp, scale, hp, op)
+        status = _library().ss2d_linear_attention_step(a, c.handle)
+        if status:
+            _check(status, "ss2d_linear_attention_step")
     return out
 
 

@@ -41,20 +41,28 @@ __global__ void __launch_bounds__(kLrThreads) linear_recurrent_kernel(const LinA
 
     if (!STEP && blockIdx.x == 0 && tid == 0)
         *a.err = 0;  // nothing here waits
+
+    // one token's q, k, v and log decay: loads that are on their way before they are needed
+    float q_in = 0.0f, k_in = 0.0f, g = 0.0f;
+    uint2 v_in = make_uint2(0, 0);
+    auto fetch = [&](long long rb, long long rt) {
+        if (tid < a.Dk) {
+            q_in = __bfloat162float(a.q[rb * a.q_batch + rt * a.q_token + group * a.q_head + tid]);
+            k_in = __bfloat162float(a.k[rb * a.k_batch + rt * a.k_token + group * a.k_head + tid]);
+        }
+        if (cols)
+            v_in = *reinterpret_cast<const uint2 *>(a.v + rb * a.v_batch + rt * a.v_token + h * a.v_head + c);
+        g = a.log_decay[a.per_token ? (rb * (STEP ? 1 : a.L) + rt) * a.H + h : h];
+    };
+    if (STEP)
+        fetch(b, 0);
     long long slot = b;
     int count = a.L;
-    if (STEP) {
-        if (a.slots) {
-            slot = a.slots[b];
-            if (slot < 0 || slot >= a.pool)
-                return;
-            bool earlier = false;
-            for (int i = tid; i < b; i += kLrThreads)
-                earlier |= a.slots[i] == (int)slot;
-            if (__syncthreads_or(earlier))
-                return;
-        }
-    } else if (a.lengths) {
+    if (STEP && a.slots) {
+        slot = a.slots[b];
+        if (slot < 0 || slot >= a.pool)
+            return;
+    } else if (!STEP && a.lengths) {
         count = min(max(a.lengths[b], 0), a.L);
     }
 
@@ -68,23 +76,44 @@ __global__ void __launch_bounds__(kLrThreads) linear_recurrent_kernel(const LinA
             s[i] = *reinterpret_cast<const float4 *>(a.h0 + at + (size_t)r * a.Dv + c);
     }
 
+    // the first row of this slot after `from`; a.B if there is none
+    auto find_next = [&](int from) {
+        for (int i = from + 1 + tid; i < a.B; i += kLrThreads)
+            if (a.slots[i] == (int)slot) {
+                atomicMin(&next_row, i);
+                break;
+            }
+    };
+    if (STEP && a.slots) {
+        // (while the state is on its way)
+        if (tid == 0)
+            next_row = a.B;
+        __syncthreads();
+        find_next(b);
+        bool earlier = false;
+        for (int i = tid; i < b; i += kLrThreads)
+            earlier |= a.slots[i] == (int)slot;
+        if (__syncthreads_or(earlier))
+            return;
+    }
+
+    if (!STEP && count > 0)
+        fetch(b, 0);
     int row = STEP ? b : 0;
     while (STEP || row < count) {
         const long long rb = STEP ? row : b, rt = STEP ? 0 : row;
         if (tid < a.Dk) {
-            sq[tid] = __bfloat162float(a.q[rb * a.q_batch + rt * a.q_token + group * a.q_head + tid]) * a.scale;
-            sk[tid] = __bfloat162float(a.k[rb * a.k_batch + rt * a.k_token + group * a.k_head + tid]);
+            sq[tid] = q_in * a.scale;
+            sk[tid] = k_in;
         }
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (cols) {
-            const uint2 w = *reinterpret_cast<const uint2 *>(a.v + rb * a.v_batch + rt * a.v_token + h * a.v_head + c);
-            v = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
-                            __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
-        }
-        const float g = a.log_decay[a.per_token ? (rb * (STEP ? 1 : a.L) + rt) * a.H + h : h];
-        const float decay = expf(la_clamp(g));
-        if (STEP && a.slots && tid == 0)
-            next_row = a.B;
+        const float4 v = make_float4(__uint_as_float(v_in.x << 16), __uint_as_float(v_in.x & 0xffff0000u),
+                                     __uint_as_float(v_in.y << 16), __uint_as_float(v_in.y & 0xffff0000u));
+        // exp(g) = keep + grow: 1 and a small number for slow decays, whose rounding to fp32 would otherwise add up
+        // over the tokens, else 0 and the decay itself
+        const bool slow = g > -0.5f;
+        const float keep = slow ? 1.0f : 0.0f, grow = slow ? expm1f(g) : expf(la_clamp(g));
+        if (!STEP && row + 1 < count)
+            fetch(b, row + 1);
         __syncthreads();
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
@@ -92,10 +121,10 @@ __global__ void __launch_bounds__(kLrThreads) linear_recurrent_kernel(const LinA
             const int r = r0 + i * kLrGroups;
             if (r < a.Dk) {
                 const float kr = sk[r], qr = sq[r];
-                s[i].x = fmaf(s[i].x, decay, kr * v.x);
-                s[i].y = fmaf(s[i].y, decay, kr * v.y);
-                s[i].z = fmaf(s[i].z, decay, kr * v.z);
-                s[i].w = fmaf(s[i].w, decay, kr * v.w);
+                s[i].x = fmaf(s[i].x, keep, fmaf(s[i].x, grow, kr * v.x));
+                s[i].y = fmaf(s[i].y, keep, fmaf(s[i].y, grow, kr * v.y));
+                s[i].z = fmaf(s[i].z, keep, fmaf(s[i].z, grow, kr * v.z));
+                s[i].w = fmaf(s[i].w, keep, fmaf(s[i].w, grow, kr * v.w));
                 o.x = fmaf(qr, s[i].x, o.x);
                 o.y = fmaf(qr, s[i].y, o.y);
                 o.z = fmaf(qr, s[i].z, o.z);
@@ -112,16 +141,6 @@ __global__ void __launch_bounds__(kLrThreads) linear_recurrent_kernel(const LinA
         }
         if (lane < kLrCols / 4)
             *reinterpret_cast<float4 *>(&part[tid / 32][lane * 4]) = o;
-        if (STEP && a.slots) {
-            int next = a.B;
-            for (int i = row + 1 + tid; i < a.B; i += kLrThreads)
-                if (a.slots[i] == (int)slot) {
-                    next = i;
-                    break;
-                }
-            if (next < a.B)
-                atomicMin(&next_row, next);
-        }
         __syncthreads();
         if (tid < kLrCols && slice * kLrCols + tid < a.Dv) {
             float y = 0.0f;
@@ -134,7 +153,12 @@ __global__ void __launch_bounds__(kLrThreads) linear_recurrent_kernel(const LinA
             if (!a.slots || next_row >= a.B)
                 break;
             row = next_row;
+            fetch(row, 0);
             __syncthreads();
+            if (tid == 0)
+                next_row = a.B;
+            __syncthreads();
+            find_next(row);  // (the loop's next barrier stands before it is read)
         } else {
             ++row;
         }

@@ -7,7 +7,8 @@
 //   residual_out = r                              rounded to the residual's type
 //
 // A row stays in registers between the reduction of its squares and the output, so each
-// tensor is read or written once: the kernel is bounded by device memory.
+// tensor is read or written once: the kernel is bounded by device memory, and what matters is to keep
+// enough loads in flight and the instructions few.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <stddef.h>
@@ -36,112 +37,178 @@ struct RmsArgs {
     float eps;
 };
 
-__device__ __forceinline__ float rn_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float rn_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// Eight consecutive elements, 16-byte aligned, as they lie in memory.
+template <bool BF16>
+struct Raw8 {
+    static constexpr int kPieces = BF16 ? 1 : 2;
+    uint4 v[kPieces];
 
-// Eight consecutive elements from column c on as fp32; columns past D are zero.  VEC: D % 8 == 0,
-// so the eight are in range together and 16-byte aligned.
-template <bool VEC>
-__device__ __forceinline__ void rn_load8(const void *base, bool bf16, long long row, int D, int c, float (&f)[8])
-{
-    if (VEC) {
-        if (bf16) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(base) + row * D + c));
-            f[0] = rn_lo(v.x), f[1] = rn_hi(v.x), f[2] = rn_lo(v.y), f[3] = rn_hi(v.y);
-            f[4] = rn_lo(v.z), f[5] = rn_hi(v.z), f[6] = rn_lo(v.w), f[7] = rn_hi(v.w);
-        } else {
-            const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + row * D + c);
-            const float4 a = __ldg(p), b = __ldg(p + 1);
-            f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-            f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-        }
-    } else {
+    __device__ __forceinline__ void load(const void *base, long long i)
+    {
+        const uint4 *p = BF16 ? reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(base) + i)
+                              : reinterpret_cast<const uint4 *>(static_cast<const float *>(base) + i);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const long long at = row * D + c + i;
-            f[i] = c + i >= D ? 0.0f
-                   : bf16     ? __bfloat162float(static_cast<const __nv_bfloat16 *>(base)[at])
-                              : static_cast<const float *>(base)[at];
-        }
+        for (int x = 0; x < kPieces; ++x)
+            v[x] = __ldg(p + x);
     }
-}
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int x = 0; x < kPieces; ++x)
+            v[x] = make_uint4(0, 0, 0, 0);
+    }
+    // elements 2 i and 2 i + 1
+    __device__ __forceinline__ float2 pair(int i) const
+    {
+        const uint4 hi = v[kPieces - 1];
+        const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, hi.x, hi.y, hi.z, hi.w};
+        return BF16 ? make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u))
+                    : make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    }
+};
 
-__device__ __forceinline__ uint32_t rn_pack(float lo, float hi)
+__device__ __forceinline__ uint32_t rn_pack(float2 f)
 {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    const __nv_bfloat162 v = __floats2bfloat162_rn(f.x, f.y);
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-template <bool VEC>
-__device__ __forceinline__ void rn_store8(void *base, int dtype, long long row, int D, int c, const float (&f)[8])
+__device__ __forceinline__ uint32_t rn_pack_e4m3(float2 lo, float2 hi)
 {
-    if (VEC) {
-        if (dtype == SS2D_BF16) {
-            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(base) + row * D + c) =
-                make_uint4(rn_pack(f[0], f[1]), rn_pack(f[2], f[3]), rn_pack(f[4], f[5]), rn_pack(f[6], f[7]));
-        } else if (dtype == SS2D_F32) {
-            float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(base) + row * D + c);
-            p[0] = make_float4(f[0], f[1], f[2], f[3]);
-            p[1] = make_float4(f[4], f[5], f[6], f[7]);
-        } else {
-            uint32_t w[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                w[h] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(f[4 * h], f[4 * h + 1]), __NV_SATFINITE, __NV_E4M3) |
-                       (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(f[4 * h + 2], f[4 * h + 3]), __NV_SATFINITE,
-                                                          __NV_E4M3)
-                           << 16;
-            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(base) + row * D + c) = make_uint2(w[0], w[1]);
-        }
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3) |
+           (uint32_t)__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3) << 16;
+}
+
+__device__ __forceinline__ void rn_store8(void *base, int dtype, long long at, const float2 (&f)[4])
+{
+    if (dtype == SS2D_BF16) {
+        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(base) + at) =
+            make_uint4(rn_pack(f[0]), rn_pack(f[1]), rn_pack(f[2]), rn_pack(f[3]));
+    } else if (dtype == SS2D_F32) {
+        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(base) + at);
+        p[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+        p[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
     } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (c + i >= D)
-                break;
-            const long long at = row * D + c + i;
-            if (dtype == SS2D_BF16)
-                static_cast<__nv_bfloat16 *>(base)[at] = __float2bfloat16_rn(f[i]);
-            else if (dtype == SS2D_F32)
-                static_cast<float *>(base)[at] = f[i];
-            else
-                static_cast<uint8_t *>(base)[at] = __nv_cvt_float_to_fp8(f[i], __NV_SATFINITE, __NV_E4M3);
-        }
+        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(base) + at) =
+            make_uint2(rn_pack_e4m3(f[0], f[1]), rn_pack_e4m3(f[2], f[3]));
     }
 }
 
-// TPR threads hold a row, each NV runs of 8 columns: run t + i * TPR of thread t.  A group of
-// 128 columns is then 16 neighbouring lanes of one run index.
-template <int TPR, int NV, bool VEC>
+template <bool BF16>
+__device__ __forceinline__ float rn_load(const void *base, long long at)
+{
+    return BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(base)[at]) : static_cast<const float *>(base)[at];
+}
+
+__device__ __forceinline__ void rn_store(void *base, int dtype, long long at, float f)
+{
+    if (dtype == SS2D_BF16)
+        static_cast<__nv_bfloat16 *>(base)[at] = __float2bfloat16_rn(f);
+    else if (dtype == SS2D_F32)
+        static_cast<float *>(base)[at] = f;
+    else
+        static_cast<uint8_t *>(base)[at] = __nv_cvt_float_to_fp8(f, __NV_SATFINITE, __NV_E4M3);
+}
+
+// The scale of a group, from the maximum over LANES neighbouring lanes.
+template <int LANES>
+__device__ __forceinline__ float rn_scale(float amax)
+{
+#pragma unroll
+    for (int d = LANES / 2; d > 0; d /= 2)
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+    return fmaxf(amax * (1.0f / kRnE4m3Max), kRnScaleMin);
+}
+
+// TPR threads hold a row, each 8 NV of its columns.
+//   VEC (D % 8 == 0, rows 16-byte aligned): NV runs of 8 neighbouring columns, run t + i * TPR of thread
+//   t; a group of 128 columns is one run of 16 neighbouring lanes.
+//   else (TPR a multiple of 32): single columns, a warp's 256 NV next to one another and 32 of them in
+//   the lanes, so that accesses of rows of any alignment stay together; a group is four of a warp's 32.
+// The types of x and the residual are the template's, so that all of a thread's loads are issued before
+// the first is used.  y is (r weight) rstd, and q is (r weight) (rstd / s): with the arithmetic in pairs
+// (f32x2) a column takes about eight instructions, which the loads hide.
+enum { kRnNone, kRnF32, kRnBf16 };
+
+template <int TPR, int NV, bool VEC, bool XBF16, int RES>
 __global__ void __launch_bounds__(TPR > kRnThreads ? TPR : kRnThreads) rms_norm_kernel(const RmsArgs a)
 {
     constexpr int kThreads = TPR > kRnThreads ? TPR : kRnThreads;
     constexpr int kRows = kThreads / TPR;
+    constexpr bool kResBf16 = RES == kRnBf16;
+    constexpr int kResType = kResBf16 ? SS2D_BF16 : SS2D_F32;
     const int t = threadIdx.x % TPR;
     const long long row = (long long)blockIdx.x * kRows + threadIdx.x / TPR;
     const bool live = row < a.rows;
-    float r[NV][8];
-    float sum = 0.0f;
+    const long long at = row * a.D;
+    const int first = t / 32 * (256 * NV) + t % 32;  // (single columns)
+    const bool e4m3 = a.y_dtype == SS2D_E4M3;
+    float2 r[NV][4];
+    Raw8<false> weight[VEC ? NV : 1];
+    if (VEC) {
+        Raw8<XBF16> x[NV];
+        Raw8<kResBf16> e[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (t + i * TPR) * 8;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            r[i][j] = 0.0f;
-        if (live && c < a.D) {
-            rn_load8<VEC>(a.x, a.x_bf16, row, a.D, c, r[i]);
-            if (a.residual) {
-                float e[8];
-                rn_load8<VEC>(a.residual, a.res_bf16, row, a.D, c, e);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    r[i][j] += e[j];
-                rn_store8<VEC>(a.residual_out, a.res_bf16 ? SS2D_BF16 : SS2D_F32, row, a.D, c, r[i]);
+        for (int i = 0; i < NV; ++i) {
+            x[i].clear();
+            e[i].clear();
+            if (live && (t + i * TPR) * 8 < a.D) {
+                x[i].load(a.x, at + (t + i * TPR) * 8);
+                if (RES)
+                    e[i].load(a.residual, at + (t + i * TPR) * 8);
             }
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            sum = fmaf(r[i][j], r[i][j], sum);
+        for (int i = 0; i < NV; ++i) {
+            weight[i].clear();
+            if ((t + i * TPR) * 8 < a.D)
+                weight[i].load(a.weight, (t + i * TPR) * 8);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                r[i][j] = x[i].pair(j);
+                if (RES)
+                    r[i][j] = __fadd2_rn(r[i][j], e[i].pair(j));
+            }
+            if (RES && live && (t + i * TPR) * 8 < a.D)
+                rn_store8(a.residual_out, kResType, at + (t + i * TPR) * 8, r[i]);
+        }
+    } else {
+        float f[NV][8], e[NV][8];
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = first + (8 * i + j) * 32;
+                const bool in = live && c < a.D;
+                f[i][j] = in ? rn_load<XBF16>(a.x, at + c) : 0.0f;
+                if (RES)
+                    e[i][j] = in ? rn_load<kResBf16>(a.residual, at + c) : 0.0f;
+            }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (RES)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int c = first + (8 * i + j) * 32;
+                    f[i][j] += e[i][j];
+                    if (live && c < a.D)
+                        rn_store(a.residual_out, kResType, at + c, f[i][j]);
+                }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                r[i][j] = make_float2(f[i][2 * j], f[i][2 * j + 1]);
+        }
     }
+    float2 squares = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            squares = __ffma2_rn(r[i][j], r[i][j], squares);
+    float sum = squares.x + squares.y;
 #pragma unroll
     for (int d = (TPR < 32 ? TPR : 32) / 2; d > 0; d /= 2)
         sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -151,53 +218,85 @@ __global__ void __launch_bounds__(TPR > kRnThreads ? TPR : kRnThreads) rms_norm_
         if (threadIdx.x % 32 == 0)
             part[threadIdx.x / 32] = sum;
         __syncthreads();
-        const int first = threadIdx.x / TPR * kWarps;
+        const int from = threadIdx.x / TPR * kWarps;
         sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < kWarps; ++i)
-            sum += part[first + i];
+            sum += part[from + i];
     }
     const float rstd = rsqrtf(sum / (float)a.D + a.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (t + i * TPR) * 8;
-        const bool in = live && c < a.D;
-        float w[8];
-        if (in)
-            rn_load8<VEC>(a.weight, false, 0, a.D, c, w);
+        if (VEC) {
+            const int c = (t + i * TPR) * 8;
+            const bool in = live && c < a.D;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            r[i][j] = in ? r[i][j] * rstd * w[j] : 0.0f;
-        if (a.y_dtype == SS2D_E4M3) {
-            float amax = 0.0f;
+            for (int j = 0; j < 4; ++j)
+                r[i][j] = __fmul2_rn(r[i][j], weight[i].pair(j));
+            float k = rstd;
+            if (e4m3) {
+                float amax = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                amax = fmaxf(amax, fabsf(r[i][j]));
+                for (int j = 0; j < 4; ++j)
+                    amax = fmaxf(amax, fmaxf(fabsf(r[i][j].x), fabsf(r[i][j].y)));
+                const float s = rn_scale<16>(amax * rstd);
+                k = __fdividef(rstd, s);
+                if (in && c % kRnGroup == 0)
+                    a.scales[row * a.groups + c / kRnGroup] = s;
+            }
 #pragma unroll
-            for (int d = 8; d > 0; d /= 2)
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-            const float s = fmaxf(amax / kRnE4m3Max, kRnScaleMin);
-            if (in && c % kRnGroup == 0)
-                a.scales[row * a.groups + c / kRnGroup] = s;
+            for (int j = 0; j < 4; ++j)
+                r[i][j] = __fmul2_rn(r[i][j], make_float2(k, k));
+            if (in)
+                rn_store8(a.y, a.y_dtype, at + c, r[i]);
+        } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                r[i][j] /= s;
+            for (int h = 0; h < 4; h += 2) {
+                const int c = first + (8 * i + 2 * h) * 32;  // this lane's column in the group's first 32
+                float f[4] = {r[i][h].x, r[i][h].y, r[i][h + 1].x, r[i][h + 1].y};
+                float amax = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    f[j] = c + j * 32 < a.D ? f[j] * __ldg(a.weight + c + j * 32) : 0.0f;
+                    amax = fmaxf(amax, fabsf(f[j]));
+                }
+                float k = rstd;
+                if (e4m3) {
+                    const float s = rn_scale<32>(amax * rstd);
+                    k = __fdividef(rstd, s);
+                    if (live && t % 32 == 0 && c < a.D)
+                        a.scales[row * a.groups + c / kRnGroup] = s;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (live && c + j * 32 < a.D)
+                        rn_store(a.y, a.y_dtype, at + c + j * 32, f[j] * k);
+            }
         }
-        if (in)
-            rn_store8<VEC>(a.y, a.y_dtype, row, a.D, c, r[i]);
     }
+}
+
+template <int TPR, int NV, bool VEC, bool XBF16>
+cudaError_t rms_launch_types(const RmsArgs &a, cudaStream_t s)
+{
+    constexpr int kThreads = TPR > kRnThreads ? TPR : kRnThreads;
+    const unsigned grid = (unsigned)((a.rows + kThreads / TPR - 1) / (kThreads / TPR));
+    if (!a.residual)
+        rms_norm_kernel<TPR, NV, VEC, XBF16, kRnNone><<<grid, kThreads, 0, s>>>(a);
+    else if (a.res_bf16)
+        rms_norm_kernel<TPR, NV, VEC, XBF16, kRnBf16><<<grid, kThreads, 0, s>>>(a);
+    else
+        rms_norm_kernel<TPR, NV, VEC, XBF16, kRnF32><<<grid, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
 }
 
 template <int TPR, int NV>
 cudaError_t rms_launch(const RmsArgs &a, cudaStream_t s)
 {
-    constexpr int kThreads = TPR > kRnThreads ? TPR : kRnThreads;
-    const long long grid = (a.rows + kThreads / TPR - 1) / (kThreads / TPR);
+    constexpr int kWide = TPR < 32 ? 32 : TPR;  // single columns need whole warps
     if (a.D % 8 == 0)
-        rms_norm_kernel<TPR, NV, true><<<(unsigned)grid, kThreads, 0, s>>>(a);
-    else
-        rms_norm_kernel<TPR, NV, false><<<(unsigned)grid, kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+        return a.x_bf16 ? rms_launch_types<TPR, NV, true, true>(a, s) : rms_launch_types<TPR, NV, true, false>(a, s);
+    return a.x_bf16 ? rms_launch_types<kWide, NV, false, true>(a, s) : rms_launch_types<kWide, NV, false, false>(a, s);
 }
 
 size_t rms_esize(int dtype) { return dtype == SS2D_F32 ? 4 : dtype == SS2D_BF16 ? 2 : 1; }
@@ -260,19 +359,28 @@ extern "C" int ss2d_rms_norm(const void *x, int x_dtype, const void *residual, i
     a.y_dtype = y_dtype;
     a.eps = eps;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // Many rows: 16 columns a thread, so that each has several loads in flight and a row needs few
+    // warps.  Few rows (less than two for each SM): 8 columns a thread, the shortest way through a row.
+    const bool many = rows > 2 * 148;
     cudaError_t e;
     if (D <= 128)
         e = rms_launch<16, 1>(a, s);
     else if (D <= 256)
         e = rms_launch<32, 1>(a, s);
-    else if (D <= 1024)
-        e = rms_launch<128, 1>(a, s);
-    else if (D <= 2048)
+    else if (!many && D <= 2048)
         e = rms_launch<256, 1>(a, s);
-    else if (D <= 4096)
-        e = rms_launch<512, 1>(a, s);
-    else if (D <= 8192)
+    else if (!many && D <= 8192)
         e = rms_launch<1024, 1>(a, s);
+    else if (D <= 512)
+        e = rms_launch<32, 2>(a, s);
+    else if (D <= 1024)
+        e = rms_launch<64, 2>(a, s);
+    else if (D <= 2048)
+        e = rms_launch<128, 2>(a, s);
+    else if (D <= 4096)
+        e = rms_launch<256, 2>(a, s);
+    else if (D <= 8192)
+        e = rms_launch<512, 2>(a, s);
     else if (D <= 16384)
         e = rms_launch<1024, 2>(a, s);
     else

@@ -149,7 +149,7 @@ def _check_matmul(got, a, sa, w, sw, bias):
 def test_matmul_fp8(m, n, k, out_dtype):
     a, sa, w, sw, bias = _matmul_inputs(m, n, k, m * 7 + n * 3 + k)
     for b in (None, bias):
-        ws = torch.full((ss.matmul_fp8_workspace_size(m, n, k, out_dtype),), 255, dtype=torch.uint8, device="cuda")
+        ws = torch.full((ss.matmul_fp8_workspace_size(m, n, k),), 255, dtype=torch.uint8, device="cuda")
         got = ss.matmul_fp8(a, sa, w, sw, bias=b, out_dtype=out_dtype, workspace=ws)
         ss.check_workspace_status(ws)
         _check_matmul(got, a, sa, w, sw, b)
