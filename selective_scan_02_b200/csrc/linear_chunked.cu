@@ -29,8 +29,8 @@
 // factor, both at most 1; only the diagonal blocks need an exponential for each element.
 //
 // Where the heads of all sequences are too few for the GPU, a sequence is cut into segments: a first
-// pass sums each segment's own state (K and V only), a small kernel carries the states from segment to
-// segment, and the pass above then starts each segment from its own.
+// pass sums each segment's own state (K and V only), and the pass above starts each segment from the sum of
+// those before it, each decayed by what lies between.
 #include "api_internal.h"
 #include "launch_util.h"
 #include "linear_attention.h"
@@ -45,6 +45,7 @@ constexpr int kLcThreads = 1024;      // copy warp, MMA warp, decay warp, the st
 constexpr int kLcWeight = 4, kLcScore = 12, kLcState = 20, kLcOutput = 28;  // their first warps (8, 8, 8 and 4)
 constexpr uint32_t kLcBlock = kLcChunk * 128;  // bytes of 128 tokens by 64 columns of bf16
 constexpr int kLcParts = 3;           // of w V
+constexpr int kLcAhead = 3;           // chunks that a tile is asked for in L2 before its load
 constexpr int kLcIdlePolls = 1 << 25;  // of the copy warp, at 60 ns or more: about 2 s
 constexpr int kLcSms = 148;
 
@@ -62,7 +63,7 @@ struct alignas(16) ChunkDecay {
 
 struct ChunkedArgs {
     LinAttnArgs a;
-    float *states;       // (B * H, nseg, Dk, Dv): the segments' own states, then those before them
+    float *states;       // (B * H, nseg, Dk, Dv): the segments' own states; the last one's place holds h0
     float *decays;       // (B * H, nseg): the segments' decays
     int nseg, seg_chunks;
 };
@@ -145,6 +146,15 @@ __global__ void __launch_bounds__(kLcThreads, 1)
     const int t_end = min(len, t_first + p.seg_chunks * kLcChunk);
     if ((STATES || p.nseg == 1) && blockIdx.x == 0 && threadIdx.x == 0)
         *a.err = 0;  // the call's first kernel, long before any wait of it can run out
+    if (STATES && seg == 0 && a.h0) {
+        // a copy of h0, which the last segment of the pass to come may replace before the others have read it
+        const int per = cols / 4;
+        for (int x = threadIdx.x; x < a.Dk * per; x += kLcThreads) {
+            const long long at = (long long)(x / per) * a.Dv + c0 + x % per * 4;
+            *reinterpret_cast<float4 *>(p.states + (bh * p.nseg + p.nseg - 1) * a.Dk * a.Dv + at) =
+                *reinterpret_cast<const float4 *>(a.h0 + bh * a.Dk * a.Dv + at);
+        }
+    }
     if (t_first >= len && !(len == 0 && seg == 0 && !STATES))
         return;
     const int chunks = (t_end - t_first + kLcChunk - 1) / kLcChunk;  // 0 for an empty sequence: its state is kept
@@ -222,6 +232,12 @@ __global__ void __launch_bounds__(kLcThreads, 1)
                     for (int y = 0; y < (x == 1 ? 1 : DK / 64); ++y)
                         tc::tma_load_4d(at + y * kLcBlock, maps[x], bar(full + i), (x == 1 ? c0 : 0) + 64 * y,
                                         x == 1 ? h : group, t_first + c * kLcChunk, b);
+                    // a slot fills from L2 in half the time that it takes from device memory
+                    if (c + kLcAhead < chunks && (x == 1 || slice == 0))
+#pragma unroll
+                        for (int y = 0; y < (x == 1 ? 1 : DK / 64); ++y)
+                            tc::tma_prefetch_4d(maps[x], (x == 1 ? c0 : 0) + 64 * y, x == 1 ? h : group,
+                                                t_first + (c + kLcAhead) * kLcChunk, b);
                     next[x] = c + 1;
                     idle = false;
                 }
@@ -552,18 +568,27 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         const bool mine = row < a.Dk;  // row of S
         const int left = cols - half * kMine;  // columns in this thread, where above 0
         const long long size = (long long)a.Dk * a.Dv, in_head = (long long)row * a.Dv + c0 + half * kMine;
-        const float *const from = STATES       ? nullptr
-                                  : p.nseg > 1 ? p.states + (bh * p.nseg + seg) * size + in_head
-                                  : a.h0       ? a.h0 + bh * size + in_head
-                                               : nullptr;
         float2 s[kMine / 2];
+        auto load = [&](const float *from, float2 (&v)[kMine / 2]) {
 #pragma unroll
-        for (int x = 0; x < kMine; x += 4) {
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (from && mine && x < left)
-                v = *reinterpret_cast<const float4 *>(from + x);
-            s[x / 2] = make_float2(v.x, v.y), s[x / 2 + 1] = make_float2(v.z, v.w);
-        }
+            for (int x = 0; x < kMine; x += 4) {
+                float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (from && mine && x < left)
+                    f = *reinterpret_cast<const float4 *>(from + x);
+                v[x / 2] = make_float2(f.x, f.y), v[x / 2 + 1] = make_float2(f.z, f.w);
+            }
+        };
+        load(STATES || !a.h0 ? nullptr : (p.nseg > 1 ? p.states + (bh * p.nseg + p.nseg - 1) * size : a.h0 + bh * size) + in_head, s);
+        // the state before this segment, from the segments before it
+        if (!STATES)
+            for (int i = 0; i < seg; ++i) {
+                float2 own[kMine / 2];
+                load(p.states + (bh * p.nseg + i) * size + in_head, own);
+                const float d = p.decays[bh * p.nseg + i];
+#pragma unroll
+                for (int x = 0; x < kMine / 2; ++x)
+                    s[x] = __ffma2_rn(s[x], make_float2(d, d), own[x]);
+            }
         // the bf16 copy of S, its 16-byte pieces swizzled as TMA would
         auto publish = [&] {
             if (row < DK) {
@@ -669,41 +694,6 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         tc::tmem_free(tmem, 512);
 }
 
-// The state before each segment, from the segments' own states: thread = one element of a head's state.
-__global__ void __launch_bounds__(256) linear_carry_kernel(const ChunkedArgs p)
-{
-    const LinAttnArgs &a = p.a;
-    const int size = a.Dk * a.Dv;
-    const int per = (size + 255) / 256;
-    const long long bh = blockIdx.x / per;
-    const int at = (int)(blockIdx.x % per) * 256 + threadIdx.x;
-    if (at >= size)
-        return;
-    const int b = (int)(bh / a.H);
-    const int len = a.lengths ? min(max(a.lengths[b], 0), a.L) : a.L;
-    const int tokens = p.seg_chunks * kLcChunk;
-    const int segs = max(1, (len + tokens - 1) / tokens);  // with tokens
-    float *s = p.states + bh * p.nseg * size + at;
-    const float *decays = p.decays + bh * p.nseg;
-    float carry = a.h0 ? a.h0[bh * size + at] : 0.0f;
-    constexpr int kAhead = 8;
-    for (int i = 0; i < segs; i += kAhead) {
-        float own[kAhead], decay[kAhead];
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const bool in = i + j + 1 < segs;  // the last segment's own state is not summed
-            own[j] = in ? s[(long long)(i + j) * size] : 0.0f;
-            decay[j] = in ? decays[i + j] : 0.0f;
-        }
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            if (i + j < segs) {
-                s[(long long)(i + j) * size] = carry;
-                carry = fmaf(carry, decay[j], own[j]);
-            }
-    }
-}
-
 // Tensor map over (batch, token, head, column), boxes of 128 tokens by 64 columns of one head.
 cudaError_t lc_map(CUtensorMap *map, const __nv_bfloat16 *base, int B, int L, int heads, int D, long long batch,
                    long long token, long long head)
@@ -736,8 +726,6 @@ cudaError_t launch_width(const ChunkedArgs &p, cudaStream_t s)
             return e;
         linear_chunked_kernel<DK, true>
             <<<(unsigned)(heads * (p.nseg - 1) * slices), kLcThreads, Lc<DK>::kSmem, s>>>(q, k, v, p);
-        const long long per = ((long long)a.Dk * a.Dv + 255) / 256;
-        linear_carry_kernel<<<(unsigned)(heads * per), 256, 0, s>>>(p);
     }
     linear_chunked_kernel<DK, false>
         <<<(unsigned)(heads * p.nseg * slices), kLcThreads, Lc<DK>::kSmem, s>>>(q, k, v, p);

@@ -10,9 +10,10 @@
 // 128 x 128-byte tiles (one block of K) through a ring of stages.
 //
 // Two kernels, by which side of the MMA the tokens are on:
-//   wide_kernel   tokens along the 128 lanes, BN weight rows along the columns; persistent CTAs
-//                 walk the tiles.  A thread's row has one activation scale and its columns one weight
-//                 scale for a block, so a partial product costs one multiply-add.
+//   wide_kernel   tokens along the 128 lanes, BN weight rows along the columns.  A thread's row has one
+//                 activation scale and its columns one weight scale for a block, so a partial product
+//                 costs one multiply-add.  Persistent CTAs walk the tiles; where the tiles are too few
+//                 for the GPU, K is split over the CTAs of a cluster instead.
 //   narrow_kernel weight rows along the 128 lanes, few tokens along the columns, and K split over
 //                 the CTAs of a cluster, which add up in distributed shared memory: the weights' bytes
 //                 bound a product with few tokens, and this spreads their reading over all SMs.
@@ -33,6 +34,8 @@ constexpr int kFmBlock = 128;            // K (in bytes) of a block, a stage and
 constexpr int kFmRows = 128;             // lanes of an MMA
 constexpr uint32_t kFmTile = kFmRows * kFmBlock;  // bytes of a 128-row tile of a stage
 constexpr size_t kFmWorkspace = 256;     // the error word of the bounded waits
+constexpr int kFmMaxSplit = 8;           // CTAs of a cluster of the narrow kernel
+constexpr int kFmMaxWideSplit = 4;       // of the wide one: eight, alone on their SMs, are slow to start (5 us more)
 
 struct Fp8Args {
     const float *a_scales, *w_scales, *bias;
@@ -43,7 +46,7 @@ struct Fp8Args {
     int vec;      // wide: bytes that rows of c and their tiles are aligned to: 32, 16 or 0
     int mtiles;   // wide: tiles along M;  narrow: tiles along the tokens
     int tiles;    // of the whole product
-    int split;    // narrow: CTAs of a cluster
+    int split;    // CTAs of a cluster, each with its part of K
 };
 
 // kind::f8f6f4: fp32 accumulate, e4m3 A and B, both K-major
@@ -71,18 +74,48 @@ struct Ring {
     __device__ __forceinline__ Ring(uint32_t it, uint32_t n) : slot(it % n), round((it / n) & 1u) {}
 };
 
-// One block's MMAs: A 128 rows, B n rows, 128 bytes of K.
-__device__ __forceinline__ void fm_mma_block(uint32_t tmem, uint32_t a, uint32_t b, uint32_t idesc)
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+
+// The address of this CTA's shared memory at `addr` in the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t cluster_at(uint32_t addr, uint32_t rank)
+{
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(remote) : "r"(addr), "r"(rank));
+    return remote;
+}
+
+__device__ __forceinline__ float cluster_ld(uint32_t remote)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(remote) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float4 cluster_ld4(uint32_t remote)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(remote)
+                 : "memory");
+    return v;
+}
+
+// One block's MMAs, of one thread: A 128 rows, B n rows, 128 bytes of K.
+__device__ __forceinline__ void fm_mma_block(uint32_t tmem, uint64_t a, uint64_t b, uint32_t idesc)
 {
 #pragma unroll
     for (uint32_t k = 0; k < kFmBlock / 32; ++k)
-        tc::mma_e4m3(tmem, tc::swizzled_desc(a + 32 * k, 16, 1024), tc::swizzled_desc(b + 32 * k, 16, 1024), idesc, k > 0);
+        tc::mma_e4m3(tmem, a + 2 * k, b + 2 * k, idesc, k > 0);  // addresses in units of 16 bytes
 }
 
 // ---- wide ----------------------------------------------------------------------------------
 
 constexpr int kWideThreads = 320;  // copy warp, MMA warp, eight warps that scale and add
-constexpr int kWideSumThreads = 256;
+constexpr int kWideSumWarps = 8;
 
 template <int BN>
 struct Wide {
@@ -90,10 +123,62 @@ struct Wide {
     static constexpr int kBuffers = 512 / BN;                 // of tensor memory
     static constexpr uint32_t kStage = kFmTile + BN * kFmBlock;
     static constexpr int kCols = BN / 2;                      // columns of one summing thread
+    static constexpr uint32_t kPitch = BN * 4 + 16;           // bytes between rows of a split tile's sums
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + (2 * kStages + 2 * kBuffers) * 8 + 16;
+    static_assert(kFmRows * kPitch <= kStages * kStage, "the sums reuse the stages");
+    // CTAs of a cluster wait for one another, so none may wait for tensor memory that a CTA of another
+    // cluster holds: no two CTAs that wait so fit an SM together (the narrow kernel's need 57 KB or more)
+    static_assert(kSmem > 171 * 1024, "alone on its SM among those that wait for a cluster");
 };
 
-template <int BN>
+// Stores `n` (a multiple of 4 where vec, at least 1) neighbouring sums of a row.
+template <int N>
+__device__ __forceinline__ void fm_store(const Fp8Args &p, size_t at, const float2 (&acc)[N / 2], int n)
+{
+    if (p.c_bf16) {
+        __nv_bfloat16 *c = static_cast<__nv_bfloat16 *>(p.c) + at;
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i) {
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                w[j] = fm_pack(acc[8 * i + j].x, acc[8 * i + j].y);
+            if (p.vec == 32 && 16 * i + 16 <= n)
+                fm_store32(c + 16 * i, w);
+            else if (p.vec && 16 * i + 8 <= n) {
+                *reinterpret_cast<uint4 *>(c + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+                if (16 * i + 16 <= n)
+                    *reinterpret_cast<uint4 *>(c + 16 * i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (16 * i + 2 * j < n)
+                        c[16 * i + 2 * j] = __float2bfloat16_rn(acc[8 * i + j].x);
+                    if (16 * i + 2 * j + 1 < n)
+                        c[16 * i + 2 * j + 1] = __float2bfloat16_rn(acc[8 * i + j].y);
+                }
+            }
+        }
+    } else {
+        float *c = static_cast<float *>(p.c) + at;
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            if (p.vec && 4 * i + 4 <= n)
+                *reinterpret_cast<float4 *>(c + 4 * i) =
+                    make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
+            else {
+                const float f[4] = {acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (4 * i + j < n)
+                        c[4 * i + j] = f[j];
+            }
+        }
+    }
+}
+
+// SPLIT: one tile for each cluster, the CTA's part of K, and the parts added in distributed shared memory.
+template <int BN, bool SPLIT>
 __global__ void __launch_bounds__(kWideThreads, 1)
     matmul_fp8_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w, const Fp8Args p)
 {
@@ -106,7 +191,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     auto done = [&](uint32_t b) { return bars + 8 * (2 * W::kStages + b); };
     auto taken = [&](uint32_t b) { return bars + 8 * (2 * W::kStages + W::kBuffers + b); };
     __shared__ uint32_t tmem_slot;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < W::kStages; ++s) {
@@ -115,13 +200,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
         for (int b = 0; b < W::kBuffers; ++b) {
             tc::mbar_init(done(b), 1);
-            tc::mbar_init(taken(b), kWideSumThreads / 32);
+            tc::mbar_init(taken(b), kWideSumWarps);
         }
         tc::mbar_init_fence();
-        tc::tma_prefetch_map(&map_a);
-        tc::tma_prefetch_map(&map_w);
         if (blockIdx.x == 0)
             *p.err = 0;  // long before any wait of this call can run out
+    }
+    if (warp == 0 && tc::elect_one()) {
+        tc::tma_prefetch_map(&map_a);
+        tc::tma_prefetch_map(&map_w);
     }
     if (warp == 1)
         tc::tmem_alloc(&tmem_slot, 512);
@@ -130,13 +217,18 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     tc::fence_after();
     const uint32_t tmem = tmem_slot;
     bool good = true;
+    const int rank = SPLIT ? (int)(blockIdx.x % p.split) : 0;
+    const int first = SPLIT ? (int)(blockIdx.x / p.split) : (int)blockIdx.x;
+    const int next = SPLIT ? p.tiles : (int)gridDim.x;
+    const int kb0 = SPLIT ? (int)((long long)p.KB * rank / p.split) : 0;
+    const int kb1 = SPLIT ? (int)((long long)p.KB * (rank + 1) / p.split) : p.KB;
 
     if (warp == 0) {
         if (lane == 0) {
             uint32_t it = 0;
-            for (int tile = blockIdx.x; tile < p.tiles && good; tile += gridDim.x) {
+            for (int tile = first; tile < p.tiles && good; tile += next) {
                 const int m0 = tile % p.mtiles * kFmRows, n0 = tile / p.mtiles * BN;
-                for (int kb = 0; kb < p.KB && good; ++kb, ++it) {
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
                     const Ring r(it, W::kStages);
                     good = tc::mbar_wait(empty(r.slot), r.round ^ 1u);
                     if (!good)
@@ -152,48 +244,49 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 tc::mbar_wait(full(Ring(i, W::kStages).slot), Ring(i, W::kStages).round);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            for (int tile = blockIdx.x; tile < p.tiles && good; tile += gridDim.x)
-                for (int kb = 0; kb < p.KB && good; ++kb, ++it) {
-                    const Ring r(it, W::kStages), t(it, W::kBuffers);
-                    good = tc::mbar_wait(taken(t.slot), t.round ^ 1u) && tc::mbar_wait(full(r.slot), r.round);
-                    if (!good)
-                        break;
-                    tc::fence_after();
-                    const uint32_t a = base + r.slot * W::kStage;
-                    fm_mma_block(tmem + t.slot * BN, a, a + kFmTile, fm_idesc(BN));
+        const uint64_t a_desc = tc::swizzled_desc(base, 16, 1024), w_desc = tc::swizzled_desc(base + kFmTile, 16, 1024);
+        uint32_t it = 0;
+        for (int tile = first; tile < p.tiles && good; tile += next)
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const Ring r(it, W::kStages), t(it, W::kBuffers);
+                good = tc::mbar_wait_warp(taken(t.slot), t.round ^ 1u) && tc::mbar_wait_warp(full(r.slot), r.round);
+                if (!good)
+                    break;
+                tc::fence_after();
+                if (tc::elect_one()) {
+                    fm_mma_block(tmem + t.slot * BN, a_desc + r.slot * (W::kStage / 16), w_desc + r.slot * (W::kStage / 16),
+                                 fm_idesc(BN));
                     tc::commit(empty(r.slot));
                     tc::commit(done(t.slot));
                 }
-        }
+                __syncwarp();
+            }
     } else {
-        const int half = (warp - 2) / 4;  // of the tile's columns
+        const int group = (warp - 2) / 4;  // half of the tile's columns
         const uint32_t lanes = (uint32_t)(warp % 4) * 32;
         const int row = (int)lanes + lane;
         uint32_t it = 0;
-        for (int tile = blockIdx.x; tile < p.tiles && good; tile += gridDim.x) {
-            const int m0 = tile % p.mtiles * kFmRows, n0 = tile / p.mtiles * BN + half * W::kCols;
-            const int m = m0 + row;
+        for (int tile = first; tile < p.tiles && good; tile += next) {
+            const int m = tile % p.mtiles * kFmRows + row, n0 = tile / p.mtiles * BN + group * W::kCols;
             const float *sa = p.a_scales + (size_t)min(m, p.M - 1) * p.KB;
             const float *sw = p.w_scales + (size_t)(min(n0, p.N - 1) / kFmBlock) * p.KB;
             float2 acc[W::kCols / 2];
 #pragma unroll
             for (int i = 0; i < W::kCols / 2; ++i)
                 acc[i] = make_float2(0.0f, 0.0f);
-            float s_a = __ldg(sa), s_w = __ldg(sw);
-            for (int kb = 0; kb < p.KB && good; ++kb, ++it) {
+            float s_a = kb0 < kb1 ? __ldg(sa + kb0) : 0.0f, s_w = kb0 < kb1 ? __ldg(sw + kb0) : 0.0f;
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const Ring t(it, W::kBuffers);
                 const float s = s_a * s_w;
-                if (kb + 1 < p.KB) {  // the next block's scales, on their way meanwhile
+                if (kb + 1 < kb1) {  // the next block's scales, on their way meanwhile
                     s_a = __ldg(sa + kb + 1);
                     s_w = __ldg(sw + kb + 1);
                 }
-                good = __all_sync(0xffffffffu, tc::mbar_wait(done(t.slot), t.round));
+                good = tc::mbar_wait_warp(done(t.slot), t.round);
                 if (!good)
                     break;
                 tc::fence_after();
-                const uint32_t from = tmem + (lanes << 16) + t.slot * BN + half * W::kCols;
+                const uint32_t from = tmem + (lanes << 16) + t.slot * BN + group * W::kCols;
                 const float2 s2 = make_float2(s, s);
                 uint32_t v[2][16];
                 tc::tmem_ld16(from, v[0]);
@@ -202,20 +295,30 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     tc::tmem_wait16(v[c & 1]);
                     if (c + 1 < W::kCols / 16)
                         tc::tmem_ld16(from + 16 * (c + 1), v[(c + 1) & 1]);
+                    else {
+                        // all of the buffer is in registers
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            tc::mbar_arrive(taken(t.slot));
+                    }
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         acc[c * 8 + i] = __ffma2_rn(
                             make_float2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])), s2,
                             acc[c * 8 + i]);
                 }
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    tc::mbar_arrive(taken(t.slot));
             }
             if (!good)
                 break;
-            if (m < p.M && n0 < p.N) {
+            if (SPLIT) {
+                // the last block's MMAs are done and have read their stages: all of them are free
+                float *const sums = reinterpret_cast<float *>(smem_raw + (base - tc::smem_u32(smem_raw)));
+#pragma unroll
+                for (int i = 0; i < W::kCols / 4; ++i)
+                    *reinterpret_cast<float4 *>(sums + row * (W::kPitch / 4) + group * W::kCols + 4 * i) =
+                        make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
+            } else if (m < p.M && n0 < p.N) {
                 const int cols = min(W::kCols, p.N - n0);
                 if (p.bias)
 #pragma unroll
@@ -225,47 +328,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                         if (2 * i + 1 < cols)
                             acc[i].y += __ldg(p.bias + n0 + 2 * i + 1);
                     }
-                const size_t at = (size_t)m * p.N + n0;
-                if (p.c_bf16) {
-                    __nv_bfloat16 *c = static_cast<__nv_bfloat16 *>(p.c) + at;
-#pragma unroll
-                    for (int i = 0; i < W::kCols / 16; ++i) {
-                        uint32_t w[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            w[j] = fm_pack(acc[8 * i + j].x, acc[8 * i + j].y);
-                        if (p.vec == 32 && 16 * i + 16 <= cols)
-                            fm_store32(c + 16 * i, w);
-                        else if (p.vec && 16 * i + 8 <= cols) {
-                            *reinterpret_cast<uint4 *>(c + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
-                            if (16 * i + 16 <= cols)
-                                *reinterpret_cast<uint4 *>(c + 16 * i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                if (16 * i + 2 * j < cols)
-                                    c[16 * i + 2 * j] = __float2bfloat16_rn(acc[8 * i + j].x);
-                                if (16 * i + 2 * j + 1 < cols)
-                                    c[16 * i + 2 * j + 1] = __float2bfloat16_rn(acc[8 * i + j].y);
-                            }
-                        }
-                    }
-                } else {
-                    float *c = static_cast<float *>(p.c) + at;
-#pragma unroll
-                    for (int i = 0; i < W::kCols / 4; ++i) {
-                        if (p.vec && 4 * i + 4 <= cols)
-                            *reinterpret_cast<float4 *>(c + 4 * i) =
-                                make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
-                        else {
-                            const float f[4] = {acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y};
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                if (4 * i + j < cols)
-                                    c[4 * i + j] = f[j];
-                        }
-                    }
-                }
+                fm_store<W::kCols>(p, (size_t)m * p.N + n0, acc, cols);
             }
         }
     }
@@ -276,13 +339,64 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     __syncthreads();
     if (warp == 1)
         tc::tmem_free(tmem, 512);
+    if (SPLIT) {
+        // The cluster's CTAs add their parts of K in rank order, each for its share of the tile's rows.
+        cluster_sync();
+        if (warp >= 2) {
+            const int per = kFmRows / p.split, t = threadIdx.x - 64;
+            const int m0 = first % p.mtiles * kFmRows, n0 = first / p.mtiles * BN;
+            for (int x = t; x < per * (BN / 4); x += kWideSumWarps * 32) {
+                const int r = rank * per + x / (BN / 4), c = x % (BN / 4) * 4;
+                const int m = m0 + r, n = n0 + c;
+                if (m >= p.M || n >= p.N)
+                    continue;
+                const uint32_t at = base + r * W::kPitch + c * 4;
+                float4 part[kFmMaxWideSplit];
+#pragma unroll
+                for (int i = 0; i < kFmMaxWideSplit; ++i)
+                    if (i < p.split)
+                        part[i] = cluster_ld4(cluster_at(at, i));
+                float y[4] = {part[0].x, part[0].y, part[0].z, part[0].w};
+#pragma unroll
+                for (int i = 1; i < kFmMaxWideSplit; ++i)
+                    if (i < p.split)
+                        y[0] += part[i].x, y[1] += part[i].y, y[2] += part[i].z, y[3] += part[i].w;
+                const int left = min(4, p.N - n);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (p.bias && j < left)
+                        y[j] += __ldg(p.bias + n + j);
+                const size_t to = (size_t)m * p.N + n;
+                if (p.c_bf16) {
+                    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.c) + to;
+                    if (p.vec)
+                        *reinterpret_cast<uint2 *>(o) = make_uint2(fm_pack(y[0], y[1]), fm_pack(y[2], y[3]));
+                    else
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (j < left)
+                                o[j] = __float2bfloat16_rn(y[j]);
+                } else {
+                    float *o = static_cast<float *>(p.c) + to;
+                    if (p.vec)
+                        *reinterpret_cast<float4 *>(o) = make_float4(y[0], y[1], y[2], y[3]);
+                    else
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (j < left)
+                                o[j] = y[j];
+                }
+            }
+        }
+        __syncwarp();
+        cluster_sync();  // no CTA leaves while another reads its sums
+    }
 }
 
 // ---- narrow --------------------------------------------------------------------------------
 
 constexpr int kNarrowThreads = 192;  // copy warp, MMA warp, four warps that scale and add
 constexpr int kNarrowStages = 4;
-constexpr int kNarrowMaxSplit = 8;
 // 128 columns of tensor memory for a CTA and more than a quarter of an SM's shared memory, so that all
 // CTAs that fit an SM can hold their columns at once: the CTAs of a cluster wait for one another, and
 // none may wait for columns that a CTA of another cluster holds.
@@ -297,20 +411,6 @@ struct Narrow {
     static_assert(kSmem > 57 * 1024, "more than a quarter of an SM's shared memory");
     static_assert((size_t)kNarrowStages * kStage >= (size_t)BT * kFmRows * 4, "the sums reuse the stages");
 };
-
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-}
-
-__device__ __forceinline__ float cluster_ld(uint32_t addr, uint32_t rank)
-{
-    uint32_t remote;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(remote) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(remote) : "memory");
-    return v;
-}
 
 template <int BT>
 __global__ void __launch_bounds__(kNarrowThreads)
@@ -327,7 +427,7 @@ __global__ void __launch_bounds__(kNarrowThreads)
     auto done = [&](uint32_t b) { return bars + 8 * (2 * kNarrowStages + b); };
     auto taken = [&](uint32_t b) { return bars + 8 * (2 * kNarrowStages + W::kBuffers + b); };
     __shared__ uint32_t tmem_slot;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const int rank = (int)(blockIdx.x % p.split);
     const int tile = (int)(blockIdx.x / p.split);
     const int t0 = tile % p.mtiles * BT, n0 = tile / p.mtiles * kFmRows;
@@ -373,19 +473,21 @@ __global__ void __launch_bounds__(kNarrowThreads)
                 tc::mbar_wait(full(Ring(i, kNarrowStages).slot), Ring(i, kNarrowStages).round);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const Ring r(it, kNarrowStages), t(it, W::kBuffers);
-                good = tc::mbar_wait(taken(t.slot), t.round ^ 1u) && tc::mbar_wait(full(r.slot), r.round);
-                if (!good)
-                    break;
-                tc::fence_after();
-                const uint32_t w = base + r.slot * W::kStage;
-                fm_mma_block(tmem + t.slot * BT, w, w + kFmTile, fm_idesc(BT));
+        const uint64_t w_desc = tc::swizzled_desc(base, 16, 1024), a_desc = tc::swizzled_desc(base + kFmTile, 16, 1024);
+        uint32_t it = 0;
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+            const Ring r(it, kNarrowStages), t(it, W::kBuffers);
+            good = tc::mbar_wait_warp(taken(t.slot), t.round ^ 1u) && tc::mbar_wait_warp(full(r.slot), r.round);
+            if (!good)
+                break;
+            tc::fence_after();
+            if (tc::elect_one()) {
+                fm_mma_block(tmem + t.slot * BT, w_desc + r.slot * (W::kStage / 16), a_desc + r.slot * (W::kStage / 16),
+                             fm_idesc(BT));
                 tc::commit(empty(r.slot));
                 tc::commit(done(t.slot));
             }
+            __syncwarp();
         }
     } else {
         // Each warp keeps its own copy of a block's BT scales, two blocks deep.
@@ -418,7 +520,7 @@ __global__ void __launch_bounds__(kNarrowThreads)
             if (kb + 1 < kb1)
                 fetch(kb + 1);
             __syncwarp();
-            good = __all_sync(0xffffffffu, tc::mbar_wait(done(t.slot), t.round));
+            good = tc::mbar_wait_warp(done(t.slot), t.round);
             if (!good)
                 break;
             tc::fence_after();
@@ -468,13 +570,20 @@ __global__ void __launch_bounds__(kNarrowThreads)
     if (warp >= 2) {
         const int row = (warp % 4) * 32 + lane, n = n0 + row;
         const float bias = p.bias && n < p.N ? __ldg(p.bias + n) : 0.0f;
-        const int per = BT / p.split;
         const uint32_t from = base + (uint32_t)row * 4;
-        for (int t = rank * per; t < (rank + 1) * per && t0 + t < p.M; ++t) {
-            float y = 0.0f;
+        for (int t = rank; t < BT && t0 + t < p.M; t += p.split) {
+            float y;
             if (p.split > 1) {
-                for (int r = 0; r < p.split; ++r)
-                    y += cluster_ld(from + (uint32_t)t * kFmRows * 4, (uint32_t)r);
+                float part[kFmMaxSplit];
+#pragma unroll
+                for (int r = 0; r < kFmMaxSplit; ++r)
+                    if (r < p.split)
+                        part[r] = cluster_ld(cluster_at(from + (uint32_t)t * kFmRows * 4, (uint32_t)r));
+                y = part[0];
+#pragma unroll
+                for (int r = 1; r < kFmMaxSplit; ++r)
+                    if (r < p.split)
+                        y += part[r];
             } else {
                 y = sums[t * kFmRows + row];
             }
@@ -488,6 +597,7 @@ __global__ void __launch_bounds__(kNarrowThreads)
             }
         }
     }
+    __syncwarp();
     if (p.split > 1)
         cluster_sync();  // no CTA leaves while another reads its sums
 }
@@ -502,8 +612,26 @@ cudaError_t fm_map(CUtensorMap *map, const void *base, int rows, int K, int box_
     return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, sizes, strides, box);
 }
 
-template <int BN>
-cudaError_t launch_wide(const ss2d_matmul_fp8_args &g, Fp8Args p, int sms, cudaStream_t s)
+template <class Kernel>
+cudaError_t fm_launch_clusters(Kernel kernel, unsigned grid, int threads, size_t smem, int split, cudaStream_t s,
+                               const CUtensorMap &a, const CUtensorMap &w, const Fp8Args &p)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)split;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a, w, p);
+}
+
+template <int BN, bool SPLIT>
+cudaError_t launch_wide(const ss2d_matmul_fp8_args &g, Fp8Args p, int split, int sms, cudaStream_t s)
 {
     static int configured[kMaxDevices];
     CUtensorMap a, w;
@@ -511,7 +639,7 @@ cudaError_t launch_wide(const ss2d_matmul_fp8_args &g, Fp8Args p, int sms, cudaS
     if (e == cudaSuccess)
         e = fm_map(&w, g.w, g.N, g.K, BN);
     if (e == cudaSuccess)
-        e = configure_smem(matmul_fp8_wide_kernel<BN>, (int)Wide<BN>::kSmem, configured);
+        e = configure_smem(matmul_fp8_wide_kernel<BN, SPLIT>, (int)Wide<BN>::kSmem, configured);
     if (e != cudaSuccess)
         return e;
     p.mtiles = (g.M + kFmRows - 1) / kFmRows;
@@ -519,7 +647,11 @@ cudaError_t launch_wide(const ss2d_matmul_fp8_args &g, Fp8Args p, int sms, cudaS
     if (tiles > 0x7fffffff - sms)
         return cudaErrorInvalidConfiguration;
     p.tiles = (int)tiles;
-    matmul_fp8_wide_kernel<BN><<<min(p.tiles, sms), kWideThreads, Wide<BN>::kSmem, s>>>(a, w, p);
+    p.split = split;
+    if (SPLIT)
+        return fm_launch_clusters(matmul_fp8_wide_kernel<BN, SPLIT>, (unsigned)(p.tiles * split), kWideThreads,
+                                  Wide<BN>::kSmem, split, s, a, w, p);
+    matmul_fp8_wide_kernel<BN, SPLIT><<<min(p.tiles, sms), kWideThreads, Wide<BN>::kSmem, s>>>(a, w, p);
     return cudaGetLastError();
 }
 
@@ -538,18 +670,8 @@ cudaError_t launch_narrow(const ss2d_matmul_fp8_args &g, Fp8Args p, int split, c
     p.mtiles = (g.M + BT - 1) / BT;
     p.tiles = p.mtiles * ((g.N + kFmRows - 1) / kFmRows);
     p.split = split;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(p.tiles * split));
-    cfg.blockDim = dim3(kNarrowThreads);
-    cfg.dynamicSmemBytes = Narrow<BT>::kSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)split;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, matmul_fp8_narrow_kernel<BT>, a, w, p);
+    return fm_launch_clusters(matmul_fp8_narrow_kernel<BT>, (unsigned)(p.tiles * split), kNarrowThreads, Narrow<BT>::kSmem,
+                              split, s, a, w, p);
 }
 
 cudaError_t launch_matmul_fp8(const ss2d_matmul_fp8_args &g, const Fp8Args &p, cudaStream_t s)
@@ -560,18 +682,30 @@ cudaError_t launch_matmul_fp8(const ss2d_matmul_fp8_args &g, const Fp8Args &p, c
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess)
         return e;
-    const long long rows = (g.N + kFmRows - 1) / kFmRows;
-    const int bt = g.M <= 16 ? 16 : g.M <= 32 ? 32 : 64;
-    const long long tiles = rows * ((g.M + bt - 1) / bt);
-    if (tiles <= 2 * sms) {
+    const long long wrows = (g.N + kFmRows - 1) / kFmRows, mtiles = (g.M + kFmRows - 1) / kFmRows;
+    if (g.M <= 32) {
+        // The weights' bytes count: as many CTAs as two for each SM, of two blocks of K or more.  (6144 x 2048,
+        // 4 tokens: split 1, 2, 4, 8: 8.0, 6.3, 6.0, 7.2 us;  4096 x 8192: 16.9, 13.0, 10.6, 10.1 us.)
         int split = 1;
-        while (split < kNarrowMaxSplit && tiles * split * 2 <= 2 * sms && split * 2 <= p.KB)
+        while (split < kFmMaxSplit && wrows * split * 2 <= 2 * sms && split * 4 <= p.KB)
             split *= 2;
-        return bt == 16 ? launch_narrow<16>(g, p, split, s) : bt == 32 ? launch_narrow<32>(g, p, split, s)
-                                                                      : launch_narrow<64>(g, p, split, s);
+        return g.M <= 16 ? launch_narrow<16>(g, p, split, s) : launch_narrow<32>(g, p, split, s);
     }
-    const long long wide = (long long)((g.M + kFmRows - 1) / kFmRows) * ((g.N + 255) / 256);
-    return wide >= sms ? launch_wide<256>(g, p, sms, s) : launch_wide<128>(g, p, sms, s);
+    // In blocks of 128 columns: a 128 x 256 tile takes 1.5 times what a 128 x 128 one takes, and adding the parts
+    // of a split about 9 blocks (128 tokens, 4096 x 8192: 27.4, 19.5, 14.7 us for split 1, 2, 4;  512 tokens,
+    // 6144 x 2048: 15.4 us in 192 tiles of 128 columns, 12.3 us in 96 of 256).
+    auto waves = [&](long long tiles) { return (tiles + sms - 1) / sms; };
+    const long long t128 = mtiles * wrows, t256 = mtiles * ((g.N + 255) / 256);
+    long long best = 2 * waves(t128) * p.KB;
+    int split = 1;
+    for (int x = 2; x <= kFmMaxWideSplit && t128 * x <= sms && x <= p.KB; x *= 2)
+        if (2 * ((p.KB + x - 1) / x + 9) < best) {
+            best = 2 * ((p.KB + x - 1) / x + 9);
+            split = x;
+        }
+    return 3 * waves(t256) * p.KB < best ? launch_wide<256, false>(g, p, 1, sms, s)
+           : split > 1                   ? launch_wide<128, true>(g, p, split, sms, s)
+                                         : launch_wide<128, false>(g, p, 1, sms, s);
 }
 
 int fm_check(const char *call, const ss2d_matmul_fp8_args *a)

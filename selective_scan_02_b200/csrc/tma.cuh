@@ -124,6 +124,14 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+// Asks for a box in L2, ahead of its tma_load_4d.
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap *map, int x, int y, int z, int w)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global [%0, {%1, %2, %3, %4}];\n" ::"l"(map), "r"(x), "r"(y),
+                 "r"(z), "r"(w)
+                 : "memory");
+}
+
 // Descriptor of a tile of 128-byte rows with the 128-byte swizzle, as a tensor copy lays it down (the
 // tile starts on a 1024-byte boundary).  K-major: a row is 128 bytes along K, `sbo` the bytes between
 // groups of 8 rows (1024), `lbo` unused.  MN-major: a row is 128 bytes along M or N and rows follow K:
