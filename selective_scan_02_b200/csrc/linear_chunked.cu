@@ -7,7 +7,7 @@
 //   S'  = exp(c_last) S + sum_j exp(c_last - c_j) k_j v_j^T
 //
 // so a chunk is four products of 128 tokens:  Q K^T,  P V with P the masked and decayed scores,
-// Q S, and K^T (w V) with w_j = exp(c_last - c_j).  A CTA walks the chunks of 64 columns of one
+// Q S, and K^T (w V) with w_j = exp(c_last - c_j).  A CTA walks the chunks of DV columns of one
 // head's state (the columns of v, o and S do not meet) over one sequence or one segment of it.  Only
 // S' = exp(c_last) S + ... is a chain from chunk to chunk, so every step has warps of its own and
 // works on the chunk that is ready for it:
@@ -40,13 +40,12 @@ namespace ss2d {
 namespace {
 
 constexpr int kLcChunk = 128;
-constexpr int kLcCols = 64;           // columns of the state in one CTA
 constexpr int kLcThreads = 1024;      // copy warp, MMA warp, decay warp, the state's MMA warp, then the groups:
 constexpr int kLcWeight = 4, kLcScore = 12, kLcState = 20, kLcOutput = 28;  // their first warps (8, 8, 8 and 4)
 constexpr uint32_t kLcBlock = kLcChunk * 128;  // bytes of 128 tokens by 64 columns of bf16
 constexpr int kLcParts = 3;           // of w V
 constexpr int kLcAhead = 3;           // chunks that a tile is asked for in L2 before its load
-constexpr int kLcIdlePolls = 1 << 25;  // of the copy warp, at 60 ns or more: about 2 s
+constexpr int kLcIdlePolls = 1 << 25;  // of a warp that polls, at 50 ns or more: about 2 s
 constexpr int kLcSms = 148;
 
 constexpr float kLcLog2e = 1.4426950408889634f, kLcLn2 = 0.6931471805599453f;
@@ -68,27 +67,34 @@ struct ChunkedArgs {
     int nseg, seg_chunks;
 };
 
-template <int DK>
+template <int DK, int DV>
 struct Lc {
     static constexpr int kSlots = DK == 64 ? 3 : 2;      // of the rings of tiles: chunks in flight
     static constexpr int kDecays = DK == 64 ? 4 : 2;     // of the ring of decays
     static constexpr uint32_t kQK = DK / 64 * kLcBlock;  // bytes of a tile of Q or K
-    static constexpr uint32_t kS = DK * 128;             // the bf16 state: DK rows of 64 columns
+    static constexpr uint32_t kW = (kLcParts * DV + 63) / 64 * kLcBlock;  // the parts of w V, next to one another
+    static constexpr uint32_t kS = DK * 128;             // the bf16 state: DK rows of up to 64 columns
     static constexpr uint32_t kQAt = 0, kKAt = kQAt + kSlots * kQK, kVAt = kKAt + kSlots * kQK,
-                              kWAt = kVAt + kSlots * kLcBlock, kSAt = kWAt + kLcParts * kLcBlock, kDecayAt = kSAt + kS,
+                              kWAt = kVAt + kSlots * kLcBlock, kSAt = kWAt + kW, kDecayAt = kSAt + kS,
                               kBarsAt = kDecayAt + kDecays * (uint32_t)sizeof(ChunkDecay);
-    // mbarriers: rings of kSlots, then pairs, then single ones
-    static constexpr int kQFull = 0, kKFull = kQFull + kSlots, kVFull = kKFull + kSlots, kQFree = kVFull + kSlots, kKFree = kQFree + kSlots,
-                         kVFree = kKFree + kSlots, kDecFull = kVFree + kSlots, kDecFree = kDecFull + kDecays,
-                         kScoresDone = kDecFree + kDecays, kProbsReady = kScoresDone + 2, kWeightsReady = kProbsReady + 2,
-                         kWeightsFree = kWeightsReady + 2, kDeltaDone = kWeightsFree + 2, kDeltaFree = kDeltaDone + 2,
-                         kOutDone = kDeltaFree + 2, kOutFree = kOutDone + 1, kStateReady = kOutFree + 1,
-                         kInterDone = kStateReady + 1, kInterFree = kInterDone + 1, kBars = kInterFree + 1;
+    // Columns of tensor memory: scores (two buffers; P in place), P V, Q S, and K^T (w V), in as many buffers as
+    // there is room for.  Of w V, all three parts in blocks of their own where they fit (one product), else the
+    // first two, and the third is added to the second's (another product).
+    static constexpr uint32_t kScoresAt = 0, kOutAt = 256, kInterAt = kOutAt + DV, kDeltaAt = kInterAt + DV;
+    static constexpr int kBlocks = kDeltaAt + kLcParts * DV <= 512 ? kLcParts : kLcParts - 1;
+    static constexpr int kDelta = kBlocks * DV, kDeltas = (512 - (int)kDeltaAt) / kDelta;
+    static_assert(kDeltas >= 1, "tensor memory");
+    // mbarriers: rings of kSlots, kDecays and kDeltas, then pairs, then single ones
+    static constexpr int kQFull = 0, kKFull = kQFull + kSlots, kVFull = kKFull + kSlots, kQFree = kVFull + kSlots,
+                         kKFree = kQFree + kSlots, kVFree = kKFree + kSlots, kDecFull = kVFree + kSlots,
+                         kDecFree = kDecFull + kDecays, kDeltaDone = kDecFree + kDecays, kDeltaFree = kDeltaDone + kDeltas,
+                         kScoresDone = kDeltaFree + kDeltas, kProbsReady = kScoresDone + 2, kWeightsReady = kProbsReady + 2,
+                         kWeightsFree = kWeightsReady + 2, kStateReady = kWeightsFree + 2, kInterDone = kStateReady + 1,
+                         kInterFree = kInterDone + 1, kOutDone = kInterFree + 1, kOutFree = kOutDone + 1,
+                         kBars = kOutFree + 1;
     static constexpr size_t kSmem = kBarsAt + kBars * 8 + 8;
     static_assert(kSmem <= 232448, "shared memory of an SM");
 };
-// Columns of tensor memory: scores (two buffers; P in place), P V, Q S, K^T (w V) (two).
-constexpr uint32_t kLcScoresAt = 0, kLcOutAt = 256, kLcInterAt = 320, kLcDeltaAt = 384;
 
 // kind::f16, fp32 accumulate, bf16 operands, 128 rows
 __host__ __device__ constexpr uint32_t lc_idesc(int n, bool a_mn_major, bool b_mn_major)
@@ -118,12 +124,12 @@ __device__ __forceinline__ void lc_store32(void *p, const uint32_t *w)
 }
 
 // STATES: the first pass over segments, which sums their own states alone.
-template <int DK, bool STATES>
+template <int DK, int DV, bool STATES>
 __global__ void __launch_bounds__(kLcThreads, 1)
     linear_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                           const __grid_constant__ CUtensorMap map_v, const ChunkedArgs p)
 {
-    using C = Lc<DK>;
+    using C = Lc<DK, DV>;
     extern __shared__ __align__(1024) unsigned char smem[];
     const LinAttnArgs &a = p.a;
     const uint32_t base = tc::smem_u32(smem);
@@ -133,14 +139,14 @@ __global__ void __launch_bounds__(kLcThreads, 1)
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
 
     const int segs = STATES ? p.nseg - 1 : p.nseg;  // the last segment's own state is not carried on
-    const int slices = (a.Dv + kLcCols - 1) / kLcCols;
+    const int slices = (a.Dv + DV - 1) / DV;
     const int slice = (int)(blockIdx.x % slices);
     const int seg = (int)(blockIdx.x / slices % segs);
     const long long bh = blockIdx.x / slices / segs;
     const int h = (int)(bh % a.H), b = (int)(bh / a.H);
     const int group = h / (a.H / a.G);
-    const int c0 = slice * kLcCols;              // this CTA's columns of v, o and S
-    const int cols = min(kLcCols, a.Dv - c0);    // a multiple of 8
+    const int c0 = slice * DV;              // this CTA's columns of v, o and S
+    const int cols = min(DV, a.Dv - c0);    // a multiple of 8
     const int len = a.lengths ? min(max(a.lengths[b], 0), a.L) : a.L;
     const int t_first = seg * p.seg_chunks * kLcChunk;
     const int t_end = min(len, t_first + p.seg_chunks * kLcChunk);
@@ -172,19 +178,21 @@ __global__ void __launch_bounds__(kLcThreads, 1)
             tc::mbar_init(bar(C::kDecFull + i), 1);
             tc::mbar_init(bar(C::kDecFree + i), STATES ? 16 : 28);  // every warp of the groups
         }
+        for (int i = 0; i < C::kDeltas; ++i) {
+            tc::mbar_init(bar(C::kDeltaDone + i), 1);
+            tc::mbar_init(bar(C::kDeltaFree + i), 8);
+        }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(bar(C::kScoresDone + i), 1);
             tc::mbar_init(bar(C::kProbsReady + i), 8);
             tc::mbar_init(bar(C::kWeightsReady + i), 8);
             tc::mbar_init(bar(C::kWeightsFree + i), 1);
-            tc::mbar_init(bar(C::kDeltaDone + i), 1);
-            tc::mbar_init(bar(C::kDeltaFree + i), 8);
         }
-        tc::mbar_init(bar(C::kOutDone), 1);
-        tc::mbar_init(bar(C::kOutFree), 4);
         tc::mbar_init(bar(C::kStateReady), 8);
         tc::mbar_init(bar(C::kInterDone), 1);
         tc::mbar_init(bar(C::kInterFree), 4);
+        tc::mbar_init(bar(C::kOutDone), 1);
+        tc::mbar_init(bar(C::kOutFree), 4);
         tc::mbar_init_fence();
     }
     if (warp == 1)
@@ -199,6 +207,12 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         good = tc::mbar_wait_warp(bar(which), parity);
         tc::fence_after();
         return good;
+    };
+    // the same, without waiting
+    auto ready = [&](int which, uint32_t parity) {
+        const bool yes = tc::mbar_test_warp(bar(which), parity);
+        tc::fence_after();
+        return yes;
     };
     auto arrive = [&](int which) {
         if (lane == 0)
@@ -263,17 +277,17 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         const uint64_t v_mn = tc::swizzled_desc(base + C::kVAt, kLcBlock, 1024);  // MN-major
         auto scores = [&](int c) {
             // the buffer is free: the P V of two chunks before, which reads P in its place, was issued before
-            const uint32_t i = c % C::kSlots;
-            if (!wait(C::kKFull + i, (c / C::kSlots) & 1) || !wait(C::kQFull + i, (c / C::kSlots) & 1))
+            const uint32_t i = c % C::kSlots, round = (c / C::kSlots) & 1, two = c & 1;
+            if (!wait(C::kKFull + i, round) || !wait(C::kQFull + i, round))
                 return;
             const uint64_t q = q_k + i * (C::kQK / 16), k = k_k + i * (C::kQK / 16);
             if (tc::elect_one()) {
 #pragma unroll
                 for (int j = 0; j < DK / 16; ++j) {
                     const uint32_t off = (j / 4 * kLcBlock + j % 4 * 32) / 16;
-                    tc::mma_bf16(tmem + kLcScoresAt + (c & 1) * 128, q + off, k + off, lc_idesc(128, false, false), j > 0);
+                    tc::mma_bf16(tmem + C::kScoresAt + two * 128, q + off, k + off, lc_idesc(128, false, false), j > 0);
                 }
-                tc::commit(bar(C::kScoresDone + (c & 1)));
+                tc::commit(bar(C::kScoresDone + two));
                 tc::commit(bar(C::kQFree + i));
                 tc::commit(bar(C::kKFree + i));
             }
@@ -284,27 +298,28 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         for (int c = 0; c < chunks && good; ++c) {
             const uint32_t i = c % C::kSlots, round = (c / C::kSlots) & 1, two = c & 1, turn = (c >> 1) & 1;
             // the next chunk's scores first, unless its tiles are still on their way
-            const bool ahead = c + 1 < chunks && tc::mbar_test_warp(bar(C::kKFull + (c + 1) % C::kSlots), ((c + 1) / C::kSlots) & 1) &&
-                               tc::mbar_test_warp(bar(C::kQFull + (c + 1) % C::kSlots), ((c + 1) / C::kSlots) & 1);
+            const int next = c + 1;
+            const uint32_t ni = next % C::kSlots, nround = (next / C::kSlots) & 1;
+            const bool ahead = next < chunks && ready(C::kKFull + ni, nround) && ready(C::kQFull + ni, nround);
             if (ahead)
-                scores(c + 1);
-            // P V; P of 16 tokens lies in the first 8 of their 16 columns of the scores.  In a chunk that is not
-            // full the weight warps clear the rows of V behind the last token.
+                scores(next);
+            // P V; P of 16 tokens lies in the first 8 of their 16 columns of the scores.  In a chunk that is not full
+            // the weight warps clear the rows of V behind the last token.
             if (!wait(C::kVFull + i, round) || !wait(C::kProbsReady + two, turn) || !wait(C::kOutFree, two ^ 1u) ||
-                (t_first + (c + 1) * kLcChunk > t_end && !wait(C::kWeightsReady, two)))
+                (t_first + next * kLcChunk > t_end && !wait(C::kWeightsReady, two)))
                 break;
             const uint64_t v = v_mn + i * (kLcBlock / 16);
             if (tc::elect_one()) {
 #pragma unroll
                 for (int j = 0; j < kLcChunk / 16; ++j)
-                    tc::mma_bf16_ta(tmem + kLcOutAt, tmem + kLcScoresAt + two * 128 + j * 16,
-                                    v + j * (2048 / 16), lc_idesc(kLcCols, false, true), j > 0);
+                    tc::mma_bf16_ta(tmem + C::kOutAt, tmem + C::kScoresAt + two * 128 + j * 16, v + j * (2048 / 16),
+                                    lc_idesc(DV, false, true), j > 0);
                 tc::commit(bar(C::kOutDone));
                 tc::commit(bar(C::kVFree + i));
             }
             __syncwarp();
-            if (!ahead && c + 1 < chunks)
-                scores(c + 1);
+            if (!ahead && next < chunks)
+                scores(next);
         }
     } else if (warp == 3) {
         const uint64_t q_k = tc::swizzled_desc(base + C::kQAt, 16, 1024);         // K-major
@@ -313,25 +328,26 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         const uint64_t s_mn = tc::swizzled_desc(base + C::kSAt, kLcBlock, 1024);
         constexpr uint32_t kStep = 2048 / 16;  // 16 tokens (or rows of S) of an MN-major tile
         for (int c = 0; c < chunks && good; ++c) {
-            const uint32_t i = c % C::kSlots, turn = c & 1;
-            const uint32_t two = c & 1;  // of the buffers of K^T (w V)
-            // K^T (w V): lanes are rows of S.  With DK = 64 the upper 64 lanes read what lies behind the tile and
-            // give rows that nobody reads.
-            if (!wait(C::kKFull + i, (c / C::kSlots) & 1) || !wait(C::kDeltaFree + two, ((c >> 1) & 1) ^ 1u))
+            const uint32_t i = c % C::kSlots, turn = c & 1, buf = c % C::kDeltas;
+            // K^T (w V): lanes are rows of S.  With DK = 64 the upper 64 lanes read what lies behind the tile and give
+            // rows that nobody reads.
+            if (!wait(C::kKFull + i, (c / C::kSlots) & 1) || !wait(C::kDeltaFree + buf, ((c / C::kDeltas) & 1) ^ 1u))
                 break;
             const uint64_t kt = k_mn + i * (C::kQK / 16);
+            const uint32_t to = tmem + C::kDeltaAt + buf * C::kDelta;
             for (int half = 0; half < 2 && wait(C::kWeightsReady + half, turn); ++half) {
                 if (tc::elect_one()) {
 #pragma unroll
-                    for (int part = 0; part < kLcParts; ++part)
-#pragma unroll
-                        for (int j = 0; j < kLcChunk / 32; ++j)
-                            tc::mma_bf16(tmem + kLcDeltaAt + two * kLcCols, kt + (half * 4 + j) * kStep,
-                                         w_mn + part * (kLcBlock / 16) + (half * 4 + j) * kStep,
-                                         lc_idesc(kLcCols, true, true), half > 0 || part > 0 || j > 0);
+                    for (int x = 0; x < kLcChunk / 32; ++x) {
+                        const uint32_t j = half * 4 + x;
+                        tc::mma_bf16(to, kt + j * kStep, w_mn + j * kStep, lc_idesc(C::kDelta, true, true), half > 0 || x > 0);
+                        if (C::kBlocks < kLcParts)
+                            tc::mma_bf16(to + (C::kBlocks - 1) * DV, kt + j * kStep,
+                                         w_mn + C::kBlocks * DV / 64 * (kLcBlock / 16) + j * kStep, lc_idesc(DV, true, true), 1);
+                    }
                     tc::commit(bar(C::kWeightsFree + half));
                     if (half) {
-                        tc::commit(bar(C::kDeltaDone + two));
+                        tc::commit(bar(C::kDeltaDone + buf));
                         tc::commit(bar(C::kKFree + i));
                     }
                 }
@@ -348,8 +364,8 @@ __global__ void __launch_bounds__(kLcThreads, 1)
             if (tc::elect_one()) {
 #pragma unroll
                 for (int j = 0; j < DK / 16; ++j)
-                    tc::mma_bf16(tmem + kLcInterAt, q + (j / 4 * kLcBlock + j % 4 * 32) / 16, s_mn + j * kStep,
-                                 lc_idesc(kLcCols, false, true), j > 0);
+                    tc::mma_bf16(tmem + C::kInterAt, q + (j / 4 * kLcBlock + j % 4 * 32) / 16, s_mn + j * kStep,
+                                 lc_idesc(DV, false, true), j > 0);
                 tc::commit(bar(C::kInterDone));
                 tc::commit(bar(C::kQFree + i));
             }
@@ -435,7 +451,7 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         if (STATES && lane == 0 && good)
             p.decays[bh * p.nseg + seg] = exp2f((float)whole);
     } else if (warp >= kLcWeight && warp < kLcScore) {
-        // V -> w V, 16 bytes at a time: the same place in three tiles.  A part is the upper 16 bits of what the
+        // V -> w V, 16 bytes at a time.  A part is the upper 16 bits of what the
         // parts before it leave, so the subtractions are exact and three parts hold all 24 bits.
         const int t = threadIdx.x - kLcWeight * 32;
         for (int c = 0; c < chunks && good; ++c) {
@@ -446,13 +462,14 @@ __global__ void __launch_bounds__(kLcThreads, 1)
             unsigned char *const tileW = smem + C::kWAt;
             if (!decays_ready(c) || !wait(C::kVFull + i, round) || (n < kLcChunk && !wait(C::kKFull + i, round)))
                 break;
+            constexpr int kPieces = DV / 8, kEach = kPieces / 4;  // of a token, and of a thread's half
             for (int half = 0; half < 2; ++half) {
-                uint4 v[2];
-                float w[2];
+                uint4 v[kEach];
+                float w[kEach];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int at = ((half * 2 + x) * 256 + t) * 16, token = at / 128;
-                    v[x] = *reinterpret_cast<const uint4 *>(tileV + at);
+                for (int x = 0; x < kEach; ++x) {
+                    const int token = half * 64 + (x * 256 + t) / kPieces, piece = t % kPieces;
+                    v[x] = *reinterpret_cast<const uint4 *>(tileV + token * 128 + ((piece ^ (token & 7)) << 4));
                     w[x] = d.f[token] * d.e[token / 32];
                     // a token behind the last: zero, whatever V holds there
                     if (token >= n)
@@ -461,8 +478,8 @@ __global__ void __launch_bounds__(kLcThreads, 1)
                 if (!wait(C::kWeightsFree + half, turn ^ 1u))
                     break;
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int at = ((half * 2 + x) * 256 + t) * 16;
+                for (int x = 0; x < kEach; ++x) {
+                    const int token = half * 64 + (x * 256 + t) / kPieces, piece = t % kPieces;
                     const uint32_t in[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
                     uint32_t part[kLcParts][4];
 #pragma unroll
@@ -478,9 +495,11 @@ __global__ void __launch_bounds__(kLcThreads, 1)
                         }
                     }
 #pragma unroll
-                    for (int z = 0; z < kLcParts; ++z)
-                        *reinterpret_cast<uint4 *>(tileW + z * kLcBlock + at) =
+                    for (int z = 0; z < kLcParts; ++z) {
+                        const int col = z * kPieces + piece;  // in pieces, eight to a block
+                        *reinterpret_cast<uint4 *>(tileW + col / 8 * kLcBlock + token * 128 + ((col % 8 ^ (token & 7)) << 4)) =
                             make_uint4(part[z][0], part[z][1], part[z][2], part[z][3]);
+                    }
                 }
                 // rows of K and V behind the last token: zero, whatever the tensors hold there, since a factor of
                 // zero would not hide a NaN.  Other warps, and the MMAs of the scores, may still read these rows
@@ -507,7 +526,7 @@ __global__ void __launch_bounds__(kLcThreads, 1)
             if (!decays_ready(c) || !wait(C::kScoresDone + two, turn2))
                 break;
             const float cb = d.cb[row];
-            const uint32_t at = lanes + kLcScoresAt + two * 128 + half * 16;
+            const uint32_t at = lanes + C::kScoresAt + two * 128 + half * 16;
             auto factors = [&](const float *from, float2 (&f)[8]) {
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
@@ -564,7 +583,7 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         }
     } else if (warp >= kLcState && warp < kLcOutput) {
         const int half = (warp - kLcState) / 4;  // of the columns
-        constexpr int kMine = kLcCols / 2;
+        constexpr int kMine = DV / 2;
         const bool mine = row < a.Dk;  // row of S
         const int left = cols - half * kMine;  // columns in this thread, where above 0
         const long long size = (long long)a.Dk * a.Dv, in_head = (long long)row * a.Dv + c0 + half * kMine;
@@ -594,7 +613,7 @@ __global__ void __launch_bounds__(kLcThreads, 1)
             if (row < DK) {
 #pragma unroll
                 for (int x = 0; x < kMine / 8; ++x)
-                    *reinterpret_cast<uint4 *>(smem + C::kSAt + row * 128 + (((half * 4 + x) ^ (row & 7)) << 4)) =
+                    *reinterpret_cast<uint4 *>(smem + C::kSAt + row * 128 + (((half * (kMine / 8) + x) ^ (row & 7)) << 4)) =
                         make_uint4(lc_pack(s[4 * x].x, s[4 * x].y), lc_pack(s[4 * x + 1].x, s[4 * x + 1].y),
                                    lc_pack(s[4 * x + 2].x, s[4 * x + 2].y), lc_pack(s[4 * x + 3].x, s[4 * x + 3].y));
             }
@@ -612,22 +631,33 @@ __global__ void __launch_bounds__(kLcThreads, 1)
             const float2 keep = make_float2(decay[decay_slot(c)].keep, decay[decay_slot(c)].keep);
             __syncwarp();
             arrive(C::kDecFree + decay_slot(c));
-            if (!wait(C::kDeltaDone + turn, (c >> 1) & 1))
+            const uint32_t buf = c % C::kDeltas;
+            if (!wait(C::kDeltaDone + buf, (c / C::kDeltas) & 1))
                 break;
 #pragma unroll
             for (int x = 0; x < kMine / 16; ++x) {
+                const uint32_t at = lanes + C::kDeltaAt + buf * C::kDelta + half * kMine + 16 * x;
                 uint32_t v[16];
-                tc::tmem_ld16(lanes + kLcDeltaAt + turn * kLcCols + half * kMine + 16 * x, v);
+                tc::tmem_ld16(at, v);
                 tc::tmem_wait16(v);
 #pragma unroll
                 for (int y = 0; y < 8; ++y)
                     s[8 * x + y] = __ffma2_rn(s[8 * x + y], keep,
                                               __ffma2_rn(s[8 * x + y], grow, make_float2(__uint_as_float(v[2 * y]),
                                                                                          __uint_as_float(v[2 * y + 1]))));
+                // the smaller parts
+#pragma unroll
+                for (int z = 1; z < C::kBlocks; ++z) {
+                    tc::tmem_ld16(at + z * DV, v);
+                    tc::tmem_wait16(v);
+#pragma unroll
+                    for (int y = 0; y < 8; ++y)
+                        s[8 * x + y] = __fadd2_rn(s[8 * x + y], make_float2(__uint_as_float(v[2 * y]), __uint_as_float(v[2 * y + 1])));
+                }
             }
             tc::fence_before();
             __syncwarp();
-            arrive(C::kDeltaFree + turn);
+            arrive(C::kDeltaFree + buf);
             if (!STATES) {
                 // Q S has read the copy that is replaced now
                 if (!wait(C::kInterDone, turn))
@@ -657,10 +687,10 @@ __global__ void __launch_bounds__(kLcThreads, 1)
                 break;
             __nv_bfloat16 *const o = a.out + (((long long)b * a.L + t) * a.H + h) * a.Dv + c0;
 #pragma unroll 1
-            for (int x = 0; x < kLcCols / 16; ++x) {
+            for (int x = 0; x < DV / 16; ++x) {
                 uint32_t u[16], v[16], w[8];
-                tc::tmem_ld16(lanes + kLcInterAt + 16 * x, u);
-                tc::tmem_ld16(lanes + kLcOutAt + 16 * x, v);
+                tc::tmem_ld16(lanes + C::kInterAt + 16 * x, u);
+                tc::tmem_ld16(lanes + C::kOutAt + 16 * x, v);
                 tc::tmem_wait16(u);
                 tc::tmem_wait16(v);
 #pragma unroll
@@ -704,7 +734,7 @@ cudaError_t lc_map(CUtensorMap *map, const __nv_bfloat16 *base, int B, int L, in
     return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, sizes, strides, box);
 }
 
-template <int DK>
+template <int DK, int DV>
 cudaError_t launch_width(const ChunkedArgs &p, cudaStream_t s)
 {
     static int configured[2][kMaxDevices];
@@ -716,26 +746,29 @@ cudaError_t launch_width(const ChunkedArgs &p, cudaStream_t s)
     if (e == cudaSuccess)
         e = lc_map(&v, a.v, a.B, a.L, a.H, a.Dv, a.v_batch, a.v_token, a.v_head);
     if (e == cudaSuccess)
-        e = configure_smem(linear_chunked_kernel<DK, false>, (int)Lc<DK>::kSmem, configured[0]);
+        e = configure_smem(linear_chunked_kernel<DK, DV, false>, (int)Lc<DK, DV>::kSmem, configured[0]);
     if (e != cudaSuccess)
         return e;
-    const long long heads = (long long)a.B * a.H, slices = (a.Dv + kLcCols - 1) / kLcCols;
+    const long long heads = (long long)a.B * a.H, slices = (a.Dv + DV - 1) / DV;
     if (p.nseg > 1) {
-        e = configure_smem(linear_chunked_kernel<DK, true>, (int)Lc<DK>::kSmem, configured[1]);
+        e = configure_smem(linear_chunked_kernel<DK, DV, true>, (int)Lc<DK, DV>::kSmem, configured[1]);
         if (e != cudaSuccess)
             return e;
-        linear_chunked_kernel<DK, true>
-            <<<(unsigned)(heads * (p.nseg - 1) * slices), kLcThreads, Lc<DK>::kSmem, s>>>(q, k, v, p);
+        linear_chunked_kernel<DK, DV, true>
+            <<<(unsigned)(heads * (p.nseg - 1) * slices), kLcThreads, Lc<DK, DV>::kSmem, s>>>(q, k, v, p);
     }
-    linear_chunked_kernel<DK, false>
-        <<<(unsigned)(heads * p.nseg * slices), kLcThreads, Lc<DK>::kSmem, s>>>(q, k, v, p);
+    linear_chunked_kernel<DK, DV, false>
+        <<<(unsigned)(heads * p.nseg * slices), kLcThreads, Lc<DK, DV>::kSmem, s>>>(q, k, v, p);
     return cudaGetLastError();
 }
+
+// Columns of the state in one CTA.
+int lc_cols(const LinAttnArgs &a) { return a.Dv <= 32 ? 32 : 64; }
 
 // Segments of a sequence: as many as fill the GPU once, of at least four chunks each.
 void lc_plan(const LinAttnArgs &a, int *nseg, int *seg_chunks)
 {
-    const long long units = (long long)a.B * a.H * ((a.Dv + kLcCols - 1) / kLcCols);
+    const long long units = (long long)a.B * a.H * ((a.Dv + lc_cols(a) - 1) / lc_cols(a));
     const int chunks = (a.L + kLcChunk - 1) / kLcChunk;
     long long n = kLcSms / units;
     n = n < 1 ? 1 : n > chunks / 4 ? (chunks / 4 > 0 ? chunks / 4 : 1) : n;
@@ -769,7 +802,9 @@ cudaError_t launch_linear_chunked(const LinAttnArgs &a, void *workspace, cudaStr
         p.decays = static_cast<float *>(workspace);
         p.states = reinterpret_cast<float *>(static_cast<char *>(workspace) + round256((size_t)heads * p.nseg * 4));
     }
-    return a.Dk <= 64 ? launch_width<64>(p, s) : launch_width<128>(p, s);
+    if (lc_cols(a) == 32)
+        return a.Dk <= 64 ? launch_width<64, 32>(p, s) : launch_width<128, 32>(p, s);
+    return a.Dk <= 64 ? launch_width<64, 64>(p, s) : launch_width<128, 64>(p, s);
 }
 
 }  // namespace ss2d
