@@ -41,4 +41,35 @@ cudaError_t configure_smem(K kernel, int bytes, int *configured)
     return cudaSuccess;
 }
 
+// Launches a kernel that may be scheduled before the work ahead of it in its stream is done
+// (programmatic dependent launch), in clusters of `cluster` CTAs.  Such a kernel calls
+// grid_wait() in every thread before it reads or writes global memory, and grid_next() when all
+// that it holds of its SM is taken, so that its own successor can be scheduled behind it.
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t s, int cluster,
+                         const A &...args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attrs[2]{};
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = (unsigned)cluster;
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+#ifdef __CUDACC__
+// Waits until the work ahead in the stream is done and its writes are visible.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+// Lets the work behind in the stream be scheduled, once every CTA of this grid has called it or ended.
+__device__ __forceinline__ void grid_next() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+#endif
+
 }  // namespace ss2d

@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(kLcThreads, 1)
     const int group = h / (a.H / a.G);
     const int c0 = slice * DV;              // this CTA's columns of v, o and S
     const int cols = min(DV, a.Dv - c0);    // a multiple of 8
+    grid_wait();
     const int len = a.lengths ? min(max(a.lengths[b], 0), a.L) : a.L;
     const int t_first = seg * p.seg_chunks * kLcChunk;
     const int t_end = min(len, t_first + p.seg_chunks * kLcChunk);
@@ -200,6 +201,7 @@ __global__ void __launch_bounds__(kLcThreads, 1)
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
+    grid_next();
     const uint32_t tmem = *tmem_slot;
     bool good = true;
     // a warp of a group: waits together
@@ -754,12 +756,13 @@ cudaError_t launch_width(const ChunkedArgs &p, cudaStream_t s)
         e = configure_smem(linear_chunked_kernel<DK, DV, true>, (int)Lc<DK, DV>::kSmem, configured[1]);
         if (e != cudaSuccess)
             return e;
-        linear_chunked_kernel<DK, DV, true>
-            <<<(unsigned)(heads * (p.nseg - 1) * slices), kLcThreads, Lc<DK, DV>::kSmem, s>>>(q, k, v, p);
+        e = launch_early(linear_chunked_kernel<DK, DV, true>, (unsigned)(heads * (p.nseg - 1) * slices), kLcThreads,
+                         Lc<DK, DV>::kSmem, s, 1, q, k, v, p);
+        if (e != cudaSuccess)
+            return e;
     }
-    linear_chunked_kernel<DK, DV, false>
-        <<<(unsigned)(heads * p.nseg * slices), kLcThreads, Lc<DK, DV>::kSmem, s>>>(q, k, v, p);
-    return cudaGetLastError();
+    return launch_early(linear_chunked_kernel<DK, DV, false>, (unsigned)(heads * p.nseg * slices), kLcThreads,
+                        Lc<DK, DV>::kSmem, s, 1, q, k, v, p);
 }
 
 // Columns of the state in one CTA.

@@ -10,6 +10,7 @@
 // row of the state) by 16 rows at a time, so that even one sequence of few heads spreads over
 // many SMs, and all of the state's loads are in flight at once.  Columns of the state do not
 // meet: o's column j needs column j of S alone.
+#include "launch_util.h"
 #include "linear_attention.h"
 
 namespace ss2d {
@@ -39,6 +40,8 @@ __global__ void __launch_bounds__(kLrThreads) linear_recurrent_kernel(const LinA
     const int r0 = tid / (kLrCols / 4);                         // and first row
     const bool cols = c < a.Dv;
 
+    grid_wait();
+    grid_next();
     if (!STEP && blockIdx.x == 0 && tid == 0)
         *a.err = 0;  // nothing here waits
 
@@ -180,11 +183,8 @@ cudaError_t launch_linear_recurrent(const LinAttnArgs &a, bool step, cudaStream_
     const long long grid = (long long)a.B * a.H * ((a.Dv + kLrCols - 1) / kLrCols);
     if (grid > 0x7fffffffLL)
         return cudaErrorInvalidConfiguration;
-    if (step)
-        linear_recurrent_kernel<true><<<(unsigned)grid, kLrThreads, 0, s>>>(a);
-    else
-        linear_recurrent_kernel<false><<<(unsigned)grid, kLrThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return step ? launch_early(linear_recurrent_kernel<true>, (unsigned)grid, kLrThreads, 0, s, 1, a)
+                : launch_early(linear_recurrent_kernel<false>, (unsigned)grid, kLrThreads, 0, s, 1, a);
 }
 
 }  // namespace ss2d

@@ -203,8 +203,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             tc::mbar_init(taken(b), kWideSumWarps);
         }
         tc::mbar_init_fence();
-        if (blockIdx.x == 0)
-            *p.err = 0;  // long before any wait of this call can run out
     }
     if (warp == 0 && tc::elect_one()) {
         tc::tma_prefetch_map(&map_a);
@@ -215,6 +213,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
+    grid_wait();
+    grid_next();
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        *p.err = 0;  // long before any wait of this call can run out
     const uint32_t tmem = tmem_slot;
     bool good = true;
     const int rank = SPLIT ? (int)(blockIdx.x % p.split) : 0;
@@ -443,14 +445,18 @@ __global__ void __launch_bounds__(kNarrowThreads)
             tc::mbar_init(taken(b), 4);
         }
         tc::mbar_init_fence();
-        if (blockIdx.x == 0)
-            *p.err = 0;
+        tc::tma_prefetch_map(&map_a);
+        tc::tma_prefetch_map(&map_w);
     }
     if (warp == 1)
         tc::tmem_alloc(&tmem_slot, kNarrowCols);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
+    grid_wait();
+    grid_next();
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        *p.err = 0;
     const uint32_t tmem = tmem_slot;
     bool good = true;
     float2 acc[BT / 2];
@@ -612,24 +618,6 @@ cudaError_t fm_map(CUtensorMap *map, const void *base, int rows, int K, int box_
     return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, sizes, strides, box);
 }
 
-template <class Kernel>
-cudaError_t fm_launch_clusters(Kernel kernel, unsigned grid, int threads, size_t smem, int split, cudaStream_t s,
-                               const CUtensorMap &a, const CUtensorMap &w, const Fp8Args &p)
-{
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)split;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a, w, p);
-}
-
 template <int BN, bool SPLIT>
 cudaError_t launch_wide(const ss2d_matmul_fp8_args &g, Fp8Args p, int split, int sms, cudaStream_t s)
 {
@@ -648,11 +636,8 @@ cudaError_t launch_wide(const ss2d_matmul_fp8_args &g, Fp8Args p, int split, int
         return cudaErrorInvalidConfiguration;
     p.tiles = (int)tiles;
     p.split = split;
-    if (SPLIT)
-        return fm_launch_clusters(matmul_fp8_wide_kernel<BN, SPLIT>, (unsigned)(p.tiles * split), kWideThreads,
-                                  Wide<BN>::kSmem, split, s, a, w, p);
-    matmul_fp8_wide_kernel<BN, SPLIT><<<min(p.tiles, sms), kWideThreads, Wide<BN>::kSmem, s>>>(a, w, p);
-    return cudaGetLastError();
+    return launch_early(matmul_fp8_wide_kernel<BN, SPLIT>, (unsigned)(SPLIT ? p.tiles * split : min(p.tiles, sms)),
+                        kWideThreads, Wide<BN>::kSmem, s, split, a, w, p);
 }
 
 template <int BT>
@@ -670,8 +655,8 @@ cudaError_t launch_narrow(const ss2d_matmul_fp8_args &g, Fp8Args p, int split, c
     p.mtiles = (g.M + BT - 1) / BT;
     p.tiles = p.mtiles * ((g.N + kFmRows - 1) / kFmRows);
     p.split = split;
-    return fm_launch_clusters(matmul_fp8_narrow_kernel<BT>, (unsigned)(p.tiles * split), kNarrowThreads, Narrow<BT>::kSmem,
-                              split, s, a, w, p);
+    return launch_early(matmul_fp8_narrow_kernel<BT>, (unsigned)(p.tiles * split), kNarrowThreads, Narrow<BT>::kSmem, s,
+                        split, a, w, p);
 }
 
 cudaError_t launch_matmul_fp8(const ss2d_matmul_fp8_args &g, const Fp8Args &p, cudaStream_t s)

@@ -15,6 +15,7 @@
 #include <stdint.h>
 
 #include "api_internal.h"
+#include "launch_util.h"
 #include "op_check.h"
 #include "ss2d.h"
 
@@ -143,6 +144,8 @@ __global__ void __launch_bounds__(TPR > kRnThreads ? TPR : kRnThreads) rms_norm_
     const long long at = row * a.D;
     const int first = t / 32 * (256 * NV) + t % 32;  // (single columns)
     const bool e4m3 = a.y_dtype == SS2D_E4M3;
+    grid_wait();
+    grid_next();
     float2 r[NV][4];
     Raw8<false> weight[VEC ? NV : 1];
     if (VEC) {
@@ -282,12 +285,9 @@ cudaError_t rms_launch_types(const RmsArgs &a, cudaStream_t s)
     constexpr int kThreads = TPR > kRnThreads ? TPR : kRnThreads;
     const unsigned grid = (unsigned)((a.rows + kThreads / TPR - 1) / (kThreads / TPR));
     if (!a.residual)
-        rms_norm_kernel<TPR, NV, VEC, XBF16, kRnNone><<<grid, kThreads, 0, s>>>(a);
-    else if (a.res_bf16)
-        rms_norm_kernel<TPR, NV, VEC, XBF16, kRnBf16><<<grid, kThreads, 0, s>>>(a);
-    else
-        rms_norm_kernel<TPR, NV, VEC, XBF16, kRnF32><<<grid, kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+        return launch_early(rms_norm_kernel<TPR, NV, VEC, XBF16, kRnNone>, grid, kThreads, 0, s, 1, a);
+    return a.res_bf16 ? launch_early(rms_norm_kernel<TPR, NV, VEC, XBF16, kRnBf16>, grid, kThreads, 0, s, 1, a)
+                      : launch_early(rms_norm_kernel<TPR, NV, VEC, XBF16, kRnF32>, grid, kThreads, 0, s, 1, a);
 }
 
 template <int TPR, int NV>
