@@ -45,7 +45,7 @@ constexpr int kLcWeight = 4, kLcScore = 12, kLcState = 20, kLcOutput = 28;  // t
 constexpr uint32_t kLcBlock = kLcChunk * 128;  // bytes of 128 tokens by 64 columns of bf16
 constexpr int kLcParts = 3;           // of w V
 constexpr int kLcAhead = 3;           // chunks that a tile is asked for in L2 before its load
-constexpr int kLcIdlePolls = 1 << 25;  // of a warp that polls, at 50 ns or more: about 2 s
+constexpr int kLcIdlePolls = 1 << 24;  // of the copy warp, at 120 ns or more: about 2 s
 constexpr int kLcSms = 148;
 
 constexpr float kLcLog2e = 1.4426950408889634f, kLcLn2 = 0.6931471805599453f;
@@ -94,6 +94,19 @@ struct Lc {
                          kBars = kOutFree + 1;
     static constexpr size_t kSmem = kBarsAt + kBars * 8 + 8;
     static_assert(kSmem <= 232448, "shared memory of an SM");
+};
+
+// A chunk's place in a ring of N slots, and the parity of its round; no division as the chunks go by.
+template <int N>
+struct LcRing {
+    uint32_t slot = 0, round = 0;
+    __device__ __forceinline__ void operator++()
+    {
+        if (N == 1 || ++slot == N) {
+            slot = 0;
+            round ^= 1u;
+        }
+    }
 };
 
 // kind::f16, fp32 accumulate, bf16 operands, 128 rows
@@ -220,8 +233,6 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         if (lane == 0)
             tc::mbar_arrive(bar(which));
     };
-    auto decay_slot = [&](int c) { return c % C::kDecays; };
-    auto decays_ready = [&](int c) { return wait(C::kDecFull + decay_slot(c), (c / C::kDecays) & 1); };
     const int quarter = warp % 4;                // of the 128 lanes of tensor memory
     const uint32_t lanes = tmem + ((uint32_t)quarter << 21);
     const int row = quarter * 32 + lane;
@@ -263,7 +274,7 @@ __global__ void __launch_bounds__(kLcThreads, 1)
                     break;
                 }
                 if (idle)
-                    __nanosleep(20);
+                    __nanosleep(64);
             }
             // copies must have landed before the CTA's shared memory goes
 #pragma unroll
@@ -277,9 +288,11 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         const uint64_t q_k = tc::swizzled_desc(base + C::kQAt, 16, 1024);         // K-major
         const uint64_t k_k = tc::swizzled_desc(base + C::kKAt, 16, 1024);
         const uint64_t v_mn = tc::swizzled_desc(base + C::kVAt, kLcBlock, 1024);  // MN-major
+        LcRing<C::kSlots> tiles, ahead_of;  // of P V, and of the scores
         auto scores = [&](int c) {
             // the buffer is free: the P V of two chunks before, which reads P in its place, was issued before
-            const uint32_t i = c % C::kSlots, round = (c / C::kSlots) & 1, two = c & 1;
+            const uint32_t i = ahead_of.slot, round = ahead_of.round, two = c & 1;
+            ++ahead_of;
             if (!wait(C::kKFull + i, round) || !wait(C::kQFull + i, round))
                 return;
             const uint64_t q = q_k + i * (C::kQK / 16), k = k_k + i * (C::kQK / 16);
@@ -297,12 +310,12 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         };
         if (chunks > 0)
             scores(0);
-        for (int c = 0; c < chunks && good; ++c) {
-            const uint32_t i = c % C::kSlots, round = (c / C::kSlots) & 1, two = c & 1, turn = (c >> 1) & 1;
+        for (int c = 0; c < chunks && good; ++c, ++tiles) {
+            const uint32_t i = tiles.slot, round = tiles.round, two = c & 1, turn = (c >> 1) & 1;
             // the next chunk's scores first, unless its tiles are still on their way
             const int next = c + 1;
-            const uint32_t ni = next % C::kSlots, nround = (next / C::kSlots) & 1;
-            const bool ahead = next < chunks && ready(C::kKFull + ni, nround) && ready(C::kQFull + ni, nround);
+            const bool ahead = next < chunks && ready(C::kKFull + ahead_of.slot, ahead_of.round) &&
+                               ready(C::kQFull + ahead_of.slot, ahead_of.round);
             if (ahead)
                 scores(next);
             // P V; P of 16 tokens lies in the first 8 of their 16 columns of the scores.  In a chunk that is not full
@@ -329,11 +342,13 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         const uint64_t w_mn = tc::swizzled_desc(base + C::kWAt, kLcBlock, 1024);
         const uint64_t s_mn = tc::swizzled_desc(base + C::kSAt, kLcBlock, 1024);
         constexpr uint32_t kStep = 2048 / 16;  // 16 tokens (or rows of S) of an MN-major tile
-        for (int c = 0; c < chunks && good; ++c) {
-            const uint32_t i = c % C::kSlots, turn = c & 1, buf = c % C::kDeltas;
+        LcRing<C::kSlots> tiles;
+        LcRing<C::kDeltas> deltas;
+        for (int c = 0; c < chunks && good; ++c, ++tiles, ++deltas) {
+            const uint32_t i = tiles.slot, turn = c & 1, buf = deltas.slot;
             // K^T (w V): lanes are rows of S.  With DK = 64 the upper 64 lanes read what lies behind the tile and give
             // rows that nobody reads.
-            if (!wait(C::kKFull + i, (c / C::kSlots) & 1) || !wait(C::kDeltaFree + buf, ((c / C::kDeltas) & 1) ^ 1u))
+            if (!wait(C::kKFull + i, tiles.round) || !wait(C::kDeltaFree + buf, deltas.round ^ 1u))
                 break;
             const uint64_t kt = k_mn + i * (C::kQK / 16);
             const uint32_t to = tmem + C::kDeltaAt + buf * C::kDelta;
@@ -360,7 +375,7 @@ __global__ void __launch_bounds__(kLcThreads, 1)
             if (STATES)
                 continue;
             // Q S
-            if (!wait(C::kQFull + i, (c / C::kSlots) & 1) || !wait(C::kStateReady, turn) || !wait(C::kInterFree, turn ^ 1u))
+            if (!wait(C::kQFull + i, tiles.round) || !wait(C::kStateReady, turn) || !wait(C::kInterFree, turn ^ 1u))
                 break;
             const uint64_t q = q_k + i * (C::kQK / 16);
             if (tc::elect_one()) {
@@ -388,7 +403,8 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         double whole = 0.0;
         if (chunks > 0)
             fetch(0);
-        for (int c = 0; c < chunks; ++c) {
+        LcRing<C::kDecays> dec;
+        for (int c = 0; c < chunks; ++c, ++dec) {
             // cb_j, the sum from a block's end back to j, added from the end: where a weight exp(-cb) counts, cb is
             // small, and so is its rounding.  The same for the blocks within the chunk.
             float after[4];  // of the lane's tokens: the lane's later ones
@@ -413,9 +429,9 @@ __global__ void __launch_bounds__(kLcThreads, 1)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 blocks[q] = __shfl_sync(0xffffffffu, sum, 8 * q);
-            if (!wait(C::kDecFree + decay_slot(c), (c / C::kDecays & 1) ^ 1u))
+            if (!wait(C::kDecFree + dec.slot, dec.round ^ 1u))
                 break;
-            ChunkDecay &out = decay[decay_slot(c)];
+            ChunkDecay &out = decay[dec.slot];
             float cb[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -448,7 +464,7 @@ __global__ void __launch_bounds__(kLcThreads, 1)
             }
             whole += all;
             __syncwarp();
-            arrive(C::kDecFull + decay_slot(c));
+            arrive(C::kDecFull + dec.slot);
         }
         if (STATES && lane == 0 && good)
             p.decays[bh * p.nseg + seg] = exp2f((float)whole);
@@ -456,13 +472,15 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         // V -> w V, 16 bytes at a time.  A part is the upper 16 bits of what the
         // parts before it leave, so the subtractions are exact and three parts hold all 24 bits.
         const int t = threadIdx.x - kLcWeight * 32;
-        for (int c = 0; c < chunks && good; ++c) {
-            const uint32_t i = c % C::kSlots, round = (c / C::kSlots) & 1, turn = c & 1;
+        LcRing<C::kSlots> tiles;
+        LcRing<C::kDecays> dec;
+        for (int c = 0; c < chunks && good; ++c, ++tiles, ++dec) {
+            const uint32_t i = tiles.slot, round = tiles.round, turn = c & 1;
             const int n = min(kLcChunk, t_end - t_first - c * kLcChunk);
-            const ChunkDecay &d = decay[decay_slot(c)];
+            const ChunkDecay &d = decay[dec.slot];
             unsigned char *const tileV = smem + C::kVAt + i * kLcBlock;
             unsigned char *const tileW = smem + C::kWAt;
-            if (!decays_ready(c) || !wait(C::kVFull + i, round) || (n < kLcChunk && !wait(C::kKFull + i, round)))
+            if (!wait(C::kDecFull + dec.slot, dec.round) || !wait(C::kVFull + i, round) || (n < kLcChunk && !wait(C::kKFull + i, round)))
                 break;
             constexpr int kPieces = DV / 8, kEach = kPieces / 4;  // of a token, and of a thread's half
             for (int half = 0; half < 2; ++half) {
@@ -517,15 +535,15 @@ __global__ void __launch_bounds__(kLcThreads, 1)
                 arrive(C::kWeightsReady + half);
             }
             arrive(C::kVFree + i);
-            arrive(C::kDecFree + decay_slot(c));
+            arrive(C::kDecFree + dec.slot);
         }
     } else if (warp >= kLcScore && warp < kLcState && !STATES) {
         const int half = (warp - kLcScore) / 4;  // 16 of a block's 32 columns
-        for (int c = 0; c < chunks; ++c) {
-            const uint32_t i = c % C::kSlots, round = (c / C::kSlots) & 1;
+        LcRing<C::kDecays> dec;
+        for (int c = 0; c < chunks; ++c, ++dec) {
             const uint32_t two = c & 1, turn2 = (c >> 1) & 1;  // of the scores' two buffers
-            const ChunkDecay &d = decay[decay_slot(c)];
-            if (!decays_ready(c) || !wait(C::kScoresDone + two, turn2))
+            const ChunkDecay &d = decay[dec.slot];
+            if (!wait(C::kDecFull + dec.slot, dec.round) || !wait(C::kScoresDone + two, turn2))
                 break;
             const float cb = d.cb[row];
             const uint32_t at = lanes + C::kScoresAt + two * 128 + half * 16;
@@ -581,7 +599,7 @@ __global__ void __launch_bounds__(kLcThreads, 1)
             tc::fence_before();
             __syncwarp();
             arrive(C::kProbsReady + two);
-            arrive(C::kDecFree + decay_slot(c));
+            arrive(C::kDecFree + dec.slot);
         }
     } else if (warp >= kLcState && warp < kLcOutput) {
         const int half = (warp - kLcState) / 4;  // of the columns
@@ -625,16 +643,18 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         };
         if (!STATES)
             publish();
-        for (int c = 0; c < chunks; ++c) {
+        LcRing<C::kDecays> dec;
+        LcRing<C::kDeltas> deltas;
+        for (int c = 0; c < chunks; ++c, ++dec, ++deltas) {
             const uint32_t turn = c & 1;
-            if (!decays_ready(c))
+            if (!wait(C::kDecFull + dec.slot, dec.round))
                 break;
-            const float2 grow = make_float2(decay[decay_slot(c)].grow, decay[decay_slot(c)].grow);
-            const float2 keep = make_float2(decay[decay_slot(c)].keep, decay[decay_slot(c)].keep);
+            const float2 grow = make_float2(decay[dec.slot].grow, decay[dec.slot].grow);
+            const float2 keep = make_float2(decay[dec.slot].keep, decay[dec.slot].keep);
             __syncwarp();
-            arrive(C::kDecFree + decay_slot(c));
-            const uint32_t buf = c % C::kDeltas;
-            if (!wait(C::kDeltaDone + buf, (c / C::kDeltas) & 1))
+            arrive(C::kDecFree + dec.slot);
+            const uint32_t buf = deltas.slot;
+            if (!wait(C::kDeltaDone + buf, deltas.round))
                 break;
 #pragma unroll
             for (int x = 0; x < kMine / 16; ++x) {
@@ -677,14 +697,15 @@ __global__ void __launch_bounds__(kLcThreads, 1)
                     *reinterpret_cast<float4 *>(to + x) = make_float4(s[x / 2].x, s[x / 2].y, s[x / 2 + 1].x, s[x / 2 + 1].y);
     } else if (warp >= kLcOutput && !STATES) {
         const bool wide = a.Dv % 16 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
-        for (int c = 0; c < chunks; ++c) {
+        LcRing<C::kDecays> dec;
+        for (int c = 0; c < chunks; ++c, ++dec) {
             const uint32_t turn = c & 1;
             const int t = t_first + c * kLcChunk + row;
-            if (!decays_ready(c))
+            if (!wait(C::kDecFull + dec.slot, dec.round))
                 break;
-            const float r = a.scale * lc_ex2(decay[decay_slot(c)].cb[row] + decay[decay_slot(c)].m[quarter]);
+            const float r = a.scale * lc_ex2(decay[dec.slot].cb[row] + decay[dec.slot].m[quarter]);
             __syncwarp();
-            arrive(C::kDecFree + decay_slot(c));
+            arrive(C::kDecFree + dec.slot);
             if (!wait(C::kInterDone, turn) || !wait(C::kOutDone, turn))
                 break;
             __nv_bfloat16 *const o = a.out + (((long long)b * a.L + t) * a.H + h) * a.Dv + c0;

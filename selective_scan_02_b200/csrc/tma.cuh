@@ -50,17 +50,21 @@ __device__ __forceinline__ bool elect_one()
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t mbar, uint32_t phase)
 {
     uint32_t done;
-    int left = (int)kSpinLimit;
-    do {
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}\n"
-            : "=r"(done)
-            : "r"(mbar), "r"(phase)
-            : "memory");
-    } while (!__all_sync(0xffffffffu, done) && --left);
-    return left != 0;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, %3;\n"
+        "WAIT:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 q, n, 0;\n\t"
+        "@q bra WAIT;\n"
+        "DONE:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(mbar), "r"(phase), "n"((uint32_t)kSpinLimit)
+        : "memory");
+    return __all_sync(0xffffffffu, done);
 }
 
 // Whether the phase has completed.
