@@ -47,6 +47,7 @@ constexpr int kLcParts = 3;           // of w V
 constexpr int kLcAhead = 3;           // chunks that a tile is asked for in L2 before its load
 constexpr int kLcIdlePolls = 1 << 24;  // of the copy warp, at 120 ns or more: about 2 s
 constexpr int kLcSms = 148;
+constexpr int kLcMaxSegments = 64;
 
 constexpr float kLcLog2e = 1.4426950408889634f, kLcLn2 = 0.6931471805599453f;
 
@@ -789,14 +790,25 @@ cudaError_t launch_width(const ChunkedArgs &p, cudaStream_t s)
 // Columns of the state in one CTA.
 int lc_cols(const LinAttnArgs &a) { return a.Dv <= 32 ? 32 : 64; }
 
-// Segments of a sequence: as many as fill the GPU once, of at least four chunks each.
+// Segments of a sequence, by the time they take in chunks: both passes' waves of CTAs, with three chunks to fill and
+// drain a CTA (the first pass takes 0.8 of the second's time), and half a chunk for each segment's state that the
+// last one has to add up.  (16 heads of
+// 128 x 128, 2048 tokens, 1 to 4 segments: 36, 37, 31, 28 us;  one head of 128 x 64, 65536 tokens, 8, 16, 36,
+// 72 segments: 212, 124, 92, 105 us.)
 void lc_plan(const LinAttnArgs &a, int *nseg, int *seg_chunks)
 {
     const long long units = (long long)a.B * a.H * ((a.Dv + lc_cols(a) - 1) / lc_cols(a));
     const int chunks = (a.L + kLcChunk - 1) / kLcChunk;
-    long long n = kLcSms / units;
-    n = n < 1 ? 1 : n > chunks / 4 ? (chunks / 4 > 0 ? chunks / 4 : 1) : n;
-    *seg_chunks = (int)((chunks + n - 1) / n);
+    long long best = 0;
+    for (int n = 1; n <= kLcMaxSegments && n <= chunks; ++n) {
+        const int each = (chunks + n - 1) / n;
+        const long long waves = (units * n + kLcSms - 1) / kLcSms, first = (units * (n - 1) + kLcSms - 1) / kLcSms;
+        const long long cost = (10 * waves + 8 * first) * (each + 3) + (n > 1 ? 20 + 5 * n : 0);
+        if (n == 1 || cost < best) {
+            best = cost;
+            *seg_chunks = each;
+        }
+    }
     *nseg = (chunks + *seg_chunks - 1) / *seg_chunks;
 }
 
