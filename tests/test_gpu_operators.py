@@ -6,7 +6,7 @@ Bounds count roundings (operator_reference.py gives half a step of each type):
   - an output rounded once adds half a step of its type;
   - linear attention multiplies bf16 by bf16 on the tensor cores: the decayed scores and the carried
     state are rounded to bf16 for that (one half-step of the terms' absolute sum each), while the state
-    itself is summed from v times its decay in two bf16 parts, which leave 2^-16 of each term."""
+    itself is summed from v times its decay in three bf16 parts, which leave 2^-24 of each term."""
 import math
 
 import pytest
@@ -211,9 +211,9 @@ def _check_attention(q, k, v, gates, scale, h0, lengths, out, h_last):
     _within(out, want, want.abs() * BF16 + size * (BF16 * 1.02) + 1e-30, "out")
     if want.norm() > 0:
         assert ((out.double() - want).norm() / want.norm()).item() <= BF16, "out"
-    # two bf16 parts of each term, at most 128 truncated additions in a chunk, two roundings for each chunk
+    # three bf16 parts of each term, at most 128 truncated additions in a chunk, two roundings for each chunk
     n = 2 * 128 + 2 * math.ceil(L / 128) + 8
-    _within(h_last, S, terms * (2.0 ** -16 + n * U) + 1e-30, "h_last")
+    _within(h_last, S, terms * (2.0 ** -24 + n * U) + 1e-30, "h_last")
     if S.norm() > 0:
         assert ((h_last.double() - S).norm() / S.norm()).item() <= 1e-5, "h_last"
 
@@ -268,6 +268,26 @@ def test_linear_attention_state_passing_and_in_place():
         assert got is h
         outs.append(o)
     _check_attention(q, k, v, gates, scale, state, None, torch.cat(outs, 1), h)
+
+
+def test_linear_attention_segments_ragged_and_in_place():
+    """Few heads, so that a sequence is cut into segments: lengths that end in the first, an inner and the last
+    one, or before the first token, with the state replaced in place."""
+    shape = (4, 4000, 1, 1, 128, 96)
+    B, L, G, H, Dk, Dv = shape
+    q, k, v, gates, scale, state = _attention_inputs(shape, 16, True, True, True)
+    gates[:, 2000:2050:7] = -math.inf
+    gates *= 0.02  # slow: what the segments carry counts
+    lengths = torch.tensor([4000, 2500, 0, 131], device="cuda", dtype=torch.int32)
+    out = torch.zeros(B, L, H, Dv, device="cuda", dtype=torch.bfloat16)
+    h = state.clone()
+    ss.linear_attention(q, k, v, gates, scale=scale, h0=h, h_last=h, lengths=lengths, out=out)
+    _check_attention(q, k, v, gates, scale, state, lengths, out, h)
+    assert torch.equal(h[2], state[2])
+    # without a state before and without the one behind
+    ss.linear_attention(q, k, v, gates, scale=scale, lengths=lengths, out=out)
+    want = ref.linear_attention(q, k, v, gates, scale, None, lengths)
+    _within(out, want[0], want[0].abs() * BF16 + want[2] * (BF16 * 1.02) + 1e-30, "out")
 
 
 def test_linear_attention_resets_and_no_decay():
@@ -372,6 +392,55 @@ def test_linear_attention_step_rows_of_one_slot_and_wild_slots():
     kept = torch.full((B, H, Dv), 2.0, device="cuda", dtype=torch.bfloat16)
     out = ss.linear_attention_step(q, k, v, gates, state, slots=slots, scale=scale, out=kept.clone())
     _check_step(q, k, v, gates, scale, before, slots, out, state, kept)
+
+
+# ---- offsets beyond 32 bits ------------------------------------------------------------------------------
+
+
+def test_rms_norm_offsets_beyond_32_bits():
+    rows, d = 2 ** 31 // 4096 + 300, 4096
+    x = torch.zeros(rows, d, device="cuda", dtype=torch.bfloat16)
+    x[-200:] = torch.randn(200, d, device="cuda", generator=_gen(51)).bfloat16()
+    w = torch.ones(d, device="cuda")
+    y, s = ss.rms_norm(x, w, out_dtype=torch.float8_e4m3fn)
+    _check_norm(x[-200:], w, None, "e4m3", (y[-200:], s[-200:]), 1e-6)
+    assert (s[:-200] == 2.0 ** -100).all()
+
+
+def test_matmul_fp8_offsets_beyond_32_bits():
+    m, n, k = 2 ** 31 // 32768 + 200, 32768, 128
+    a, sa, w, sw, _ = _matmul_inputs(m, n, k, 52)
+    got = ss.matmul_fp8(a, sa, w, sw)
+    _check_matmul(got[-150:], a[-150:], sa[-150:], w, sw, None)
+
+
+def test_linear_attention_offsets_beyond_32_bits():
+    """A reset near the end leaves little to compute for the definition."""
+    B, L, H, D, tail = 1, 2 ** 31 // (256 * 64) + 500, 256, 64, 70
+    g = _gen(53)
+    q, k = (torch.randn(B, L, 1, 8, device="cuda", generator=g).bfloat16() for _ in range(2))
+    v = torch.zeros(B, L, H, D, device="cuda", dtype=torch.bfloat16)
+    v[:, -tail:] = torch.randn(B, tail, H, D, device="cuda", generator=g).bfloat16()
+    gates = torch.full((B, L, H), -0.05, device="cuda")
+    gates[:, -tail] = -math.inf
+    out, last = ss.linear_attention(q, k, v, gates, return_last_state=True)
+    _check_attention(q[:, -tail:], k[:, -tail:], v[:, -tail:], gates[:, -tail:], 1.0, None, None, out[:, -tail:], last)
+    assert (out[:, :-tail] == 0).all()
+
+
+def test_linear_attention_step_offsets_beyond_32_bits():
+    H, D = 8, 128
+    pool = 2 ** 31 // (H * D * D) + 50
+    state = torch.zeros(pool, H, D, D, device="cuda")
+    q, k, v, gates, scale, _ = _attention_inputs((3, 1, 1, H, D, D), 54, True, False, False, lead=(3,))
+    slots = torch.tensor([pool - 1, 7, pool - 20], device="cuda", dtype=torch.int32)
+    state[slots.long()] = torch.randn(3, H, D, D, device="cuda", generator=_gen(55))
+    before = state[slots.long()].clone()
+    kept = torch.zeros(3, H, D, device="cuda", dtype=torch.bfloat16)
+    out = ss.linear_attention_step(q, k, v, gates, state, slots=slots, scale=scale)
+    _check_step(q, k, v, gates, scale, before, None, out, state[slots.long()], kept)
+    state[slots.long()] = 0
+    assert not state.any()
 
 
 # ---- together --------------------------------------------------------------------------------------------
@@ -480,6 +549,69 @@ def test_layer_on_a_given_stream():
     y2, sc2, r2 = ss.rms_norm(x, layer.w1, residual=res, out_dtype=torch.float8_e4m3fn)
     assert torch.equal(qkv, ss.matmul_fp8(y2, sc2, *layer.win)) and torch.equal(r, r2)
     assert all(torch.isfinite(t.float()).all() for t in want)
+
+
+def test_workspace_status_reports_the_error_word():
+    """Every call clears the word; a word that is set says so, and the context stays usable."""
+    a, sa, w, sw, _ = _matmul_inputs(4, 64, 128, 61)
+    ws = torch.full((ss.matmul_fp8_workspace_size(4, 64, 128),), 255, dtype=torch.uint8, device="cuda")
+    ss.matmul_fp8(a, sa, w, sw, workspace=ws)
+    ss.check_workspace_status(ws)
+    ws.view(torch.int32)[0] = 1
+    with pytest.raises(ss.Ss2dError) as e:
+        ss.check_workspace_status(ws)
+    assert e.value.name == "SS2D_ERR_DEVICE"
+    for L in (3, 200):  # token by token, and in chunks
+        q, k, v, gates, scale, _ = _attention_inputs((1, L, 1, 1, 64, 64), 62, True, False, False)
+        ws = torch.full((ss.linear_attention_workspace_size(1, L, 1, 1, 64, 64),), 255, dtype=torch.uint8, device="cuda")
+        ss.linear_attention(q, k, v, gates, workspace=ws)
+        ss.check_workspace_status(ws, stream=torch.cuda.current_stream())
+    with pytest.raises(ss.Ss2dError):
+        ss.matmul_fp8(a, sa, w, sw, workspace=ws[:16])
+
+
+def test_wrong_arguments_are_refused():
+    a, sa, w, sw, bias = _matmul_inputs(6, 40, 144, 63)
+    for bad in (dict(a_scales=sa[:, :1].contiguous()), dict(w_scales=sw.double()), dict(w=w[:, :128].contiguous()),
+                dict(bias=bias[:20]), dict(bias=bias.bfloat16()), dict(a_scales=sa.cpu()), dict(a=a.view(torch.uint8)),
+                dict(out=torch.empty(6, 41, device="cuda")), dict(out_dtype=torch.float16)):
+        args = dict(a=a, a_scales=sa, w=w, w_scales=sw)
+        with pytest.raises(ValueError):
+            ss.matmul_fp8(**(args | bad))
+    with pytest.raises(ss.Ss2dError) as e:
+        ss.matmul_fp8(a[:, :136].contiguous(), sa, w[:, :136].contiguous(), sw)
+    assert e.value.name == "SS2D_ERR_UNSUPPORTED"
+    x = torch.zeros(4, 128, device="cuda", dtype=torch.bfloat16)
+    one = torch.ones(128, device="cuda")
+    for bad in (dict(weight=one[:64]), dict(weight=one.bfloat16()), dict(residual=x.half()), dict(residual=x[:2]),
+                dict(out_dtype=torch.float16), dict(scales=torch.empty(4, 1, device="cuda")), dict(x=x.t()),
+                dict(residual_out=x), dict(x=x.half())):
+        with pytest.raises(ValueError):
+            ss.rms_norm(**(dict(x=x, weight=one) | bad))
+    with pytest.raises(ss.Ss2dError):
+        ss.rms_norm(x, one, y=x)
+    with pytest.raises(ss.Ss2dError):
+        ss.rms_norm(x[:0], one)
+    with pytest.raises(ss.Ss2dError):
+        ss.rms_norm(x, one, eps=-1.0)
+    with pytest.raises(ss.Ss2dError) as e:
+        ss.rms_norm(x.flatten()[1:-127].view(3, 128), one)
+    assert e.value.name == "SS2D_ERR_MISALIGNED"
+    q, k, v, gates, scale, state = _attention_inputs((2, 5, 1, 2, 16, 16), 64, False, True, False)
+    for bad in (dict(k=k[:, :4]), dict(v=v.float()), dict(log_decay=gates[:1]), dict(log_decay=gates.view(1, 2)),
+                dict(h0=state[:1]), dict(lengths=torch.zeros(2, device="cuda", dtype=torch.int64)),
+                dict(lengths=torch.zeros(3, device="cuda", dtype=torch.int32)), dict(q=q[0])):
+        with pytest.raises(ValueError):
+            ss.linear_attention(**(dict(q=q, k=k, v=v, log_decay=gates) | bad))
+    with pytest.raises(ss.Ss2dError):
+        ss.linear_attention(q, k, v[:, :, :1].expand(2, 5, 2, 16), gates)
+    row = dict(q=q[:, 0], k=k[:, 0], v=v[:, 0], log_decay=gates, state=state)
+    for bad in (dict(state=state.bfloat16()), dict(state=state[..., :8]), dict(slots=torch.zeros(2, device="cuda")),
+                dict(q=q), dict(state=state[0])):
+        with pytest.raises(ValueError):
+            ss.linear_attention_step(**(row | bad))
+    with pytest.raises(ss.Ss2dError):
+        ss.linear_attention_step(**(row | dict(state=state[:1])))  # fewer states than rows
 
 
 def test_repeated_calls_are_identical():
