@@ -92,8 +92,11 @@ struct Lc {
                          kScoresDone = kDeltaFree + kDeltas, kProbsReady = kScoresDone + 2, kWeightsReady = kProbsReady + 2,
                          kWeightsFree = kWeightsReady + 2, kStateReady = kWeightsFree + 2, kInterDone = kStateReady + 1,
                          kInterFree = kInterDone + 1, kOutDone = kInterFree + 1, kOutFree = kOutDone + 1,
-                         kBars = kOutFree + 1;
-    static constexpr size_t kSmem = kBarsAt + kBars * 8 + 8;
+                         kVChecked = kOutFree + 1, kBars = kVChecked + kSlots;
+    // then the place of tensor memory, and marks of chunks whose V is not finite.  A slot of V is taken after
+    // its last chunk's P V, which comes after the output of the chunk before that one.
+    static constexpr int kMarks = kSlots + 1;
+    static constexpr size_t kSmem = kBarsAt + kBars * 8 + 8 + kMarks * 4;
     static_assert(kSmem <= 232448, "shared memory of an SM");
 };
 
@@ -150,6 +153,7 @@ __global__ void __launch_bounds__(kLcThreads, 1)
     ChunkDecay *const decay = reinterpret_cast<ChunkDecay *>(smem + C::kDecayAt);
     auto bar = [&](int which) { return base + C::kBarsAt + 8 * (uint32_t)which; };
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kBarsAt + C::kBars * 8);
+    int *const marks = reinterpret_cast<int *>(tmem_slot + 2);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
 
     const int segs = STATES ? p.nseg - 1 : p.nseg;  // the last segment's own state is not carried on
@@ -188,7 +192,10 @@ __global__ void __launch_bounds__(kLcThreads, 1)
             tc::mbar_init(bar(C::kQFree + i), 2);               // the scores and Q S
             tc::mbar_init(bar(C::kKFree + i), STATES ? 1 : 2);  // the scores and the state
             tc::mbar_init(bar(C::kVFree + i), STATES ? 8 : 9);  // the weight warps and P V
+            tc::mbar_init(bar(C::kVChecked + i), 8);
         }
+        for (int i = 0; i < C::kMarks; ++i)
+            marks[i] = 0;
         for (int i = 0; i < C::kDecays; ++i) {
             tc::mbar_init(bar(C::kDecFull + i), 1);
             tc::mbar_init(bar(C::kDecFree + i), STATES ? 16 : 28);  // every warp of the groups
@@ -319,10 +326,9 @@ __global__ void __launch_bounds__(kLcThreads, 1)
                                ready(C::kQFull + ahead_of.slot, ahead_of.round);
             if (ahead)
                 scores(next);
-            // P V; P of 16 tokens lies in the first 8 of their 16 columns of the scores.  In a chunk that is not full
-            // the weight warps clear the rows of V behind the last token.
-            if (!wait(C::kVFull + i, round) || !wait(C::kProbsReady + two, turn) || !wait(C::kOutFree, two ^ 1u) ||
-                (t_first + next * kLcChunk > t_end && !wait(C::kWeightsReady, two)))
+            // P V; P of 16 tokens lies in the first 8 of their 16 columns of the scores
+            if (!wait(C::kVFull + i, round) || !wait(C::kVChecked + i, round) || !wait(C::kProbsReady + two, turn) ||
+                !wait(C::kOutFree, two ^ 1u))
                 break;
             const uint64_t v = v_mn + i * (kLcBlock / 16);
             if (tc::elect_one()) {
@@ -475,33 +481,76 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         const int t = threadIdx.x - kLcWeight * 32;
         LcRing<C::kSlots> tiles;
         LcRing<C::kDecays> dec;
-        for (int c = 0; c < chunks && good; ++c, ++tiles, ++dec) {
+        LcRing<C::kMarks> mark;
+        for (int c = 0; c < chunks && good; ++c, ++tiles, ++dec, ++mark) {
             const uint32_t i = tiles.slot, round = tiles.round, turn = c & 1;
             const int n = min(kLcChunk, t_end - t_first - c * kLcChunk);
             const ChunkDecay &d = decay[dec.slot];
             unsigned char *const tileV = smem + C::kVAt + i * kLcBlock;
             unsigned char *const tileW = smem + C::kWAt;
-            if (!wait(C::kDecFull + dec.slot, dec.round) || !wait(C::kVFull + i, round) || (n < kLcChunk && !wait(C::kKFull + i, round)))
+            if (!wait(C::kVFull + i, round) || (n < kLcChunk && !wait(C::kKFull + i, round)))
                 break;
             constexpr int kPieces = DV / 8, kEach = kPieces / 4;  // of a token, and of a thread's half
+            const int piece = t % kPieces;
+            uint4 v[2][kEach];
+            __nv_bfloat162 odd = __floats2bfloat162_rn(0.0f, 0.0f);  // 0, or a NaN where an element is not finite
+#pragma unroll
+            for (int x = 0; x < 2 * kEach; ++x) {
+                const int token = (x * 256 + t) / kPieces;
+                uint4 &in = v[x / kEach][x % kEach];
+                in = *reinterpret_cast<const uint4 *>(tileV + token * 128 + ((piece ^ (token & 7)) << 4));
+                // a token behind the last: zero, whatever V holds there
+                if (token >= n)
+                    in = make_uint4(0, 0, 0, 0);
+                if (!STATES)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        odd = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&(&in.x)[y]), __floats2bfloat162_rn(0.0f, 0.0f), odd);
+            }
+            // A factor of zero does not hide an infinity or a NaN.  So rows of K and V behind the last token are zero,
+            // whatever the tensors hold there (other warps, and the MMAs of the scores, may still read these rows as
+            // they were: nothing of that reaches a row of the output or the state), and P V takes zero for such an element,
+            // which the outputs of the tokens before must not see; the output warps put a NaN in the others.
+            const bool found = !STATES && (__isnan(__low2float(odd)) || __isnan(__high2float(odd)));
+            if (found) {
+                marks[mark.slot] = c + 1;
+#pragma unroll 1
+                for (int x = 0; x < 2 * kEach * 8; ++x) {
+                    const int token = (x / 8 * 256 + t) / kPieces;
+                    unsigned short *const e = reinterpret_cast<unsigned short *>(
+                        tileV + token * 128 + ((piece ^ (token & 7)) << 4) + x % 8 * 2);
+                    if ((*e & 0x7f80) == 0x7f80)
+                        *e = 0;
+                }
+            }
+            if (n < kLcChunk)
+                for (int blk = 0; blk < (STATES ? 0 : 1) + DK / 64; ++blk) {
+                    unsigned char *const tile = blk < DK / 64 ? smem + C::kKAt + i * C::kQK + blk * kLcBlock : tileV;
+                    for (int x = t; x < (kLcChunk - n) * 8; x += 256)
+                        *reinterpret_cast<uint4 *>(tile + n * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+                }
+            if (!STATES) {
+                if (found || n < kLcChunk)
+                    tc::fence_async_proxy();
+                __syncwarp();
+                arrive(C::kVChecked + i);
+            }
+            if (!wait(C::kDecFull + dec.slot, dec.round))
+                break;
+#pragma unroll
             for (int half = 0; half < 2; ++half) {
-                uint4 v[kEach];
                 float w[kEach];
 #pragma unroll
                 for (int x = 0; x < kEach; ++x) {
-                    const int token = half * 64 + (x * 256 + t) / kPieces, piece = t % kPieces;
-                    v[x] = *reinterpret_cast<const uint4 *>(tileV + token * 128 + ((piece ^ (token & 7)) << 4));
+                    const int token = half * 64 + (x * 256 + t) / kPieces;
                     w[x] = d.f[token] * d.e[token / 32];
-                    // a token behind the last: zero, whatever V holds there
-                    if (token >= n)
-                        v[x] = make_uint4(0, 0, 0, 0);
                 }
                 if (!wait(C::kWeightsFree + half, turn ^ 1u))
                     break;
 #pragma unroll
                 for (int x = 0; x < kEach; ++x) {
-                    const int token = half * 64 + (x * 256 + t) / kPieces, piece = t % kPieces;
-                    const uint32_t in[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+                    const int token = half * 64 + (x * 256 + t) / kPieces;
+                    const uint32_t in[4] = {v[half][x].x, v[half][x].y, v[half][x].z, v[half][x].w};
                     uint32_t part[kLcParts][4];
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
@@ -522,15 +571,6 @@ __global__ void __launch_bounds__(kLcThreads, 1)
                             make_uint4(part[z][0], part[z][1], part[z][2], part[z][3]);
                     }
                 }
-                // rows of K and V behind the last token: zero, whatever the tensors hold there, since a factor of
-                // zero would not hide a NaN.  Other warps, and the MMAs of the scores, may still read these rows
-                // as they were: nothing of that reaches a row of the output or the state.
-                if (n < kLcChunk && half == 0)
-                    for (int blk = 0; blk < (STATES ? 0 : 1) + DK / 64; ++blk) {
-                        unsigned char *const tile = blk < DK / 64 ? smem + C::kKAt + i * C::kQK + blk * kLcBlock : tileV;
-                        for (int x = t; x < (kLcChunk - n) * 8; x += 256)
-                            *reinterpret_cast<uint4 *>(tile + n * 128 + x * 16) = make_uint4(0, 0, 0, 0);
-                    }
                 tc::fence_async_proxy();
                 __syncwarp();
                 arrive(C::kWeightsReady + half);
@@ -699,7 +739,8 @@ __global__ void __launch_bounds__(kLcThreads, 1)
     } else if (warp >= kLcOutput && !STATES) {
         const bool wide = a.Dv % 16 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
         LcRing<C::kDecays> dec;
-        for (int c = 0; c < chunks; ++c, ++dec) {
+        LcRing<C::kMarks> mark;
+        for (int c = 0; c < chunks; ++c, ++dec, ++mark) {
             const uint32_t turn = c & 1;
             const int t = t_first + c * kLcChunk + row;
             if (!wait(C::kDecFull + dec.slot, dec.round))
@@ -709,6 +750,7 @@ __global__ void __launch_bounds__(kLcThreads, 1)
             arrive(C::kDecFree + dec.slot);
             if (!wait(C::kInterDone, turn) || !wait(C::kOutDone, turn))
                 break;
+            const bool marked = marks[mark.slot] == c + 1;
             __nv_bfloat16 *const o = a.out + (((long long)b * a.L + t) * a.H + h) * a.Dv + c0;
 #pragma unroll 1
             for (int x = 0; x < DV / 16; ++x) {
@@ -722,6 +764,18 @@ __global__ void __launch_bounds__(kLcThreads, 1)
                     const float2 z = __ffma2_rn(make_float2(r, r), make_float2(__uint_as_float(u[2 * y]), __uint_as_float(u[2 * y + 1])),
                                                 make_float2(__uint_as_float(v[2 * y]), __uint_as_float(v[2 * y + 1])));
                     w[y] = lc_pack(z.x, z.y);
+                }
+                if (marked) {
+                    // a NaN in every column whose v, at this row's token or before it in the chunk, is not finite
+                    const __nv_bfloat16 *const from = a.v + b * a.v_batch + (t - row) * a.v_token + h * a.v_head + c0 + 16 * x;
+                    for (int j = 0; j <= row && t - row + j < t_end; ++j)
+#pragma unroll
+                        for (int y = 0; y < 8; ++y)
+                            if (16 * x + 2 * y < cols) {
+                                const uint32_t e = *reinterpret_cast<const uint32_t *>(from + j * a.v_token + 2 * y);
+                                w[y] |= ((e & 0x7f80u) == 0x7f80u ? 0x7fffu : 0u) |
+                                        ((e & 0x7f800000u) == 0x7f800000u ? 0x7fff0000u : 0u);
+                            }
                 }
                 if (t < t_end && 16 * x < cols) {
                     if (wide) {

@@ -270,6 +270,40 @@ def test_linear_attention_state_passing_and_in_place():
     _check_attention(q, k, v, gates, scale, state, None, torch.cat(outs, 1), h)
 
 
+@pytest.mark.parametrize("shape", [(1, 700, 1, 2, 128, 96), (2, 300, 1, 2, 64, 40), (1, 8, 1, 2, 16, 40),
+                                   (1, 5000, 1, 1, 32, 24)])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+def test_linear_attention_not_finite(shape, value):
+    """An infinity or a NaN reaches no token before its own, and of v no other column: all else is as without it."""
+    B, L, G, H, Dk, Dv = shape
+    q, k, v, gates, scale, state = _attention_inputs(shape, 17, True, True, False)
+    clean, clean_last = ss.linear_attention(q, k, v, gates, scale=scale, h0=state, return_last_state=True)
+    at = L // 2 + 1
+    first = torch.arange(L, device="cuda") < at
+    bad = v.clone()
+    bad[-1, at, -1, [3, Dv - 1]] = value
+    out, last = ss.linear_attention(q, k, bad, gates, scale=scale, h0=state, return_last_state=True)
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[-1, at:, -1, [3, Dv - 1]] = True
+    assert not out[hit].isfinite().any() and torch.equal(out[~hit], clean[~hit])
+    hit = torch.zeros_like(last, dtype=torch.bool)
+    hit[-1, -1, :, [3, Dv - 1]] = True
+    assert not last[hit].isfinite().any() and torch.equal(last[~hit], clean_last[~hit])
+    bad = k.clone()
+    bad[-1, at, 0, 5] = value
+    out, last = ss.linear_attention(q, bad, v, gates, scale=scale, h0=state, return_last_state=True)
+    assert not out[-1, at:].isfinite().any() and torch.equal(out[:, first], clean[:, first])
+    assert not last[-1, :, 5].isfinite().any()
+    rest = [d for d in range(Dk) if d != 5]
+    assert torch.equal(last[-1, :, rest], clean_last[-1, :, rest]) and torch.equal(last[:-1], clean_last[:-1])
+    bad = q.clone()
+    bad[-1, at, 0, 5] = value
+    out, last = ss.linear_attention(bad, k, v, gates, scale=scale, h0=state, return_last_state=True)
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[-1, at] = True
+    assert not out[hit].isfinite().any() and torch.equal(out[~hit], clean[~hit]) and torch.equal(last, clean_last)
+
+
 def test_linear_attention_segments_ragged_and_in_place():
     """Few heads, so that a sequence is cut into segments: lengths that end in the first, an inner and the last
     one, or before the first token, with the state replaced in place."""
