@@ -191,14 +191,14 @@ __global__ void __launch_bounds__(kLcThreads, 1)
             tc::mbar_init(bar(C::kVFull + i), 1);
             tc::mbar_init(bar(C::kQFree + i), 2);               // the scores and Q S
             tc::mbar_init(bar(C::kKFree + i), STATES ? 1 : 2);  // the scores and the state
-            tc::mbar_init(bar(C::kVFree + i), STATES ? 8 : 9);  // the weight warps and P V
+            tc::mbar_init(bar(C::kVFree + i), STATES ? 16 : 9);  // the weight warps and P V
             tc::mbar_init(bar(C::kVChecked + i), 8);
         }
         for (int i = 0; i < C::kMarks; ++i)
             marks[i] = 0;
         for (int i = 0; i < C::kDecays; ++i) {
             tc::mbar_init(bar(C::kDecFull + i), 1);
-            tc::mbar_init(bar(C::kDecFree + i), STATES ? 16 : 28);  // every warp of the groups
+            tc::mbar_init(bar(C::kDecFree + i), STATES ? 24 : 28);  // every warp of the groups
         }
         for (int i = 0; i < C::kDeltas; ++i) {
             tc::mbar_init(bar(C::kDeltaDone + i), 1);
@@ -475,10 +475,13 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         }
         if (STATES && lane == 0 && good)
             p.decays[bh * p.nseg + seg] = exp2f((float)whole);
-    } else if (warp >= kLcWeight && warp < kLcScore) {
+    } else if (warp >= kLcWeight && warp < (STATES ? kLcState : kLcScore)) {
         // V -> w V, 16 bytes at a time.  A part is the upper 16 bits of what the
         // parts before it leave, so the subtractions are exact and three parts hold all 24 bits.
-        const int t = threadIdx.x - kLcWeight * 32;
+        // In the first pass the score warps, which have nothing to do there, take the second half of the tokens.
+        const int t = (threadIdx.x - kLcWeight * 32) % 256;
+        constexpr int kHalves = STATES ? 1 : 2;
+        const int first = STATES ? (warp - kLcWeight) / 8 : 0;
         LcRing<C::kSlots> tiles;
         LcRing<C::kDecays> dec;
         LcRing<C::kMarks> mark;
@@ -492,11 +495,11 @@ __global__ void __launch_bounds__(kLcThreads, 1)
                 break;
             constexpr int kPieces = DV / 8, kEach = kPieces / 4;  // of a token, and of a thread's half
             const int piece = t % kPieces;
-            uint4 v[2][kEach];
+            uint4 v[kHalves][kEach];
             __nv_bfloat162 odd = __floats2bfloat162_rn(0.0f, 0.0f);  // 0, or a NaN where an element is not finite
 #pragma unroll
-            for (int x = 0; x < 2 * kEach; ++x) {
-                const int token = (x * 256 + t) / kPieces;
+            for (int x = 0; x < kHalves * kEach; ++x) {
+                const int token = first * 64 + (x * 256 + t) / kPieces;
                 uint4 &in = v[x / kEach][x % kEach];
                 in = *reinterpret_cast<const uint4 *>(tileV + token * 128 + ((piece ^ (token & 7)) << 4));
                 // a token behind the last: zero, whatever V holds there
@@ -526,8 +529,8 @@ __global__ void __launch_bounds__(kLcThreads, 1)
             if (n < kLcChunk)
                 for (int blk = 0; blk < (STATES ? 0 : 1) + DK / 64; ++blk) {
                     unsigned char *const tile = blk < DK / 64 ? smem + C::kKAt + i * C::kQK + blk * kLcBlock : tileV;
-                    for (int x = t; x < (kLcChunk - n) * 8; x += 256)
-                        *reinterpret_cast<uint4 *>(tile + n * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+                    for (int x = max(n, first * 64) * 8 + t; x < (first + kHalves) * 64 * 8; x += 256)
+                        *reinterpret_cast<uint4 *>(tile + x * 16) = make_uint4(0, 0, 0, 0);
                 }
             if (!STATES) {
                 if (found || n < kLcChunk)
@@ -538,7 +541,8 @@ __global__ void __launch_bounds__(kLcThreads, 1)
             if (!wait(C::kDecFull + dec.slot, dec.round))
                 break;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+            for (int y = 0; y < kHalves; ++y) {
+                const int half = first + y;
                 float w[kEach];
 #pragma unroll
                 for (int x = 0; x < kEach; ++x) {
@@ -550,16 +554,16 @@ __global__ void __launch_bounds__(kLcThreads, 1)
 #pragma unroll
                 for (int x = 0; x < kEach; ++x) {
                     const int token = half * 64 + (x * 256 + t) / kPieces;
-                    const uint32_t in[4] = {v[half][x].x, v[half][x].y, v[half][x].z, v[half][x].w};
+                    const uint32_t in[4] = {v[y][x].x, v[y][x].y, v[y][x].z, v[y][x].w};
                     uint32_t part[kLcParts][4];
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        float2 r = __fmul2_rn(make_float2(__uint_as_float(in[y] << 16), __uint_as_float(in[y] & 0xffff0000u)),
+                    for (int u = 0; u < 4; ++u) {
+                        float2 r = __fmul2_rn(make_float2(__uint_as_float(in[u] << 16), __uint_as_float(in[u] & 0xffff0000u)),
                                               make_float2(w[x], w[x]));
 #pragma unroll
                         for (int z = 0; z < kLcParts; ++z) {
                             const uint32_t lo = __float_as_uint(r.x), hi = __float_as_uint(r.y);
-                            part[z][y] = __byte_perm(lo, hi, 0x7632);
+                            part[z][u] = __byte_perm(lo, hi, 0x7632);
                             r = __fadd2_rn(r, make_float2(__uint_as_float((lo & 0xffff0000u) ^ 0x80000000u),
                                                           __uint_as_float((hi & 0xffff0000u) ^ 0x80000000u)));
                         }
