@@ -66,6 +66,10 @@ struct ChunkedArgs {
     float *states;       // (B * H, nseg, Dk, Dv): the segments' own states; the last one's place holds h0
     float *decays;       // (B * H, nseg): the segments' decays
     int nseg, seg_chunks;
+    // Cut units (a unit: a CTA's columns of one head of one sequence): the last `cut` ones are in two pieces, the first of
+    // which leaves its state in `states`.  CTAs take the first pieces, the whole units, then the second pieces.
+    int cut, cut_chunks;
+    int launched;        // CTAs of the launch before this one
 };
 
 template <int DK, int DV>
@@ -140,13 +144,17 @@ __device__ __forceinline__ void lc_store32(void *p, const uint32_t *w)
                  : "memory");
 }
 
-// STATES: the first pass over segments, which sums their own states alone.
-template <int DK, int DV, bool STATES>
+// What a kernel does: all of it; the first pass over segments, which sums their own states alone; or all of it with
+// cut units, whose few values more cost the other cases 3 % of their time (registers).
+enum { kLcAll, kLcStates, kLcCut };
+
+template <int DK, int DV, int PASS>
 __global__ void __launch_bounds__(kLcThreads, 1)
     linear_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                           const __grid_constant__ CUtensorMap map_v, const ChunkedArgs p)
 {
     using C = Lc<DK, DV>;
+    constexpr bool STATES = PASS == kLcStates, CUT = PASS == kLcCut;
     extern __shared__ __align__(1024) unsigned char smem[];
     const LinAttnArgs &a = p.a;
     const uint32_t base = tc::smem_u32(smem);
@@ -158,18 +166,23 @@ __global__ void __launch_bounds__(kLcThreads, 1)
 
     const int segs = STATES ? p.nseg - 1 : p.nseg;  // the last segment's own state is not carried on
     const int slices = (a.Dv + DV - 1) / DV;
-    const int slice = (int)(blockIdx.x % slices);
-    const int seg = (int)(blockIdx.x / slices % segs);
-    const long long bh = blockIdx.x / slices / segs;
+    const int place = (int)blockIdx.x + (CUT ? p.launched : 0), units = a.B * a.H * slices;
+    const bool piece0 = CUT && place < p.cut, piece1 = CUT && place >= units;
+    const int unit = !CUT ? place : piece0 ? units - p.cut + place : place - p.cut;  // with cut units: one segment
+    const int slice = unit % slices;
+    const int seg = unit / slices % segs;
+    const long long bh = unit / slices / segs;
     const int h = (int)(bh % a.H), b = (int)(bh / a.H);
     const int group = h / (a.H / a.G);
     const int c0 = slice * DV;              // this CTA's columns of v, o and S
     const int cols = min(DV, a.Dv - c0);    // a multiple of 8
-    grid_wait();
+    // Whole units behind the first launch need nothing of it, and all that they read was there before it began.
+    if (!CUT || p.launched == 0 || piece1)
+        grid_wait();
     const int len = a.lengths ? min(max(a.lengths[b], 0), a.L) : a.L;
-    const int t_first = seg * p.seg_chunks * kLcChunk;
-    const int t_end = min(len, t_first + p.seg_chunks * kLcChunk);
-    if ((STATES || p.nseg == 1) && blockIdx.x == 0 && threadIdx.x == 0)
+    const int t_first = (piece1 ? p.cut_chunks : seg * p.seg_chunks) * kLcChunk;
+    const int t_end = min(len, t_first + (piece0 ? p.cut_chunks : p.seg_chunks) * kLcChunk);
+    if ((STATES || p.nseg == 1) && place == 0 && threadIdx.x == 0)
         *a.err = 0;  // the call's first kernel, long before any wait of it can run out
     if (STATES && seg == 0 && a.h0) {
         // a copy of h0, which the last segment of the pass to come may replace before the others have read it
@@ -180,7 +193,7 @@ __global__ void __launch_bounds__(kLcThreads, 1)
                 *reinterpret_cast<const float4 *>(a.h0 + bh * a.Dk * a.Dv + at);
         }
     }
-    if (t_first >= len && !(len == 0 && seg == 0 && !STATES))
+    if (t_first >= len && !(len == 0 && seg == 0 && !piece1 && !STATES))
         return;
     const int chunks = (t_end - t_first + kLcChunk - 1) / kLcChunk;  // 0 for an empty sequence: its state is kept
 
@@ -652,6 +665,7 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         const bool mine = row < a.Dk;  // row of S
         const int left = cols - half * kMine;  // columns in this thread, where above 0
         const long long size = (long long)a.Dk * a.Dv, in_head = (long long)row * a.Dv + c0 + half * kMine;
+        float *const at_cut = p.states + ((long long)(unit - (units - p.cut)) * a.Dk + row) * DV + half * kMine;
         float2 s[kMine / 2];
         auto load = [&](const float *from, float2 (&v)[kMine / 2]) {
 #pragma unroll
@@ -662,7 +676,10 @@ __global__ void __launch_bounds__(kLcThreads, 1)
                 v[x / 2] = make_float2(f.x, f.y), v[x / 2 + 1] = make_float2(f.z, f.w);
             }
         };
-        load(STATES || !a.h0 ? nullptr : (p.nseg > 1 ? p.states + (bh * p.nseg + p.nseg - 1) * size : a.h0 + bh * size) + in_head, s);
+        load(piece1               ? at_cut
+             : STATES || !a.h0 ? nullptr
+                               : (p.nseg > 1 ? p.states + (bh * p.nseg + p.nseg - 1) * size : a.h0 + bh * size) + in_head,
+             s);
         // the state before this segment, from the segments before it
         if (!STATES)
             for (int i = 0; i < seg; ++i) {
@@ -732,6 +749,10 @@ __global__ void __launch_bounds__(kLcThreads, 1)
                 publish();
             }
         }
+        if (good && piece0 && t_end < len && mine)
+#pragma unroll
+            for (int x = 0; x < kMine; x += 4)
+                *reinterpret_cast<float4 *>(at_cut + x) = make_float4(s[x / 2].x, s[x / 2].y, s[x / 2 + 1].x, s[x / 2 + 1].y);
         float *const to = STATES                     ? p.states + (bh * p.nseg + seg) * size + in_head
                           : a.h_last && t_end == len ? a.h_last + bh * size + in_head
                                                      : nullptr;
@@ -819,7 +840,7 @@ cudaError_t lc_map(CUtensorMap *map, const __nv_bfloat16 *base, int B, int L, in
 template <int DK, int DV>
 cudaError_t launch_width(const ChunkedArgs &p, cudaStream_t s)
 {
-    static int configured[2][kMaxDevices];
+    static int configured[3][kMaxDevices];
     const LinAttnArgs &a = p.a;
     CUtensorMap q, k, v;
     cudaError_t e = lc_map(&q, a.q, a.B, a.L, a.G, a.Dk, a.q_batch, a.q_token, a.q_head);
@@ -828,20 +849,31 @@ cudaError_t launch_width(const ChunkedArgs &p, cudaStream_t s)
     if (e == cudaSuccess)
         e = lc_map(&v, a.v, a.B, a.L, a.H, a.Dv, a.v_batch, a.v_token, a.v_head);
     if (e == cudaSuccess)
-        e = configure_smem(linear_chunked_kernel<DK, DV, false>, (int)Lc<DK, DV>::kSmem, configured[0]);
+        e = p.cut ? configure_smem(linear_chunked_kernel<DK, DV, kLcCut>, (int)Lc<DK, DV>::kSmem, configured[2])
+                  : configure_smem(linear_chunked_kernel<DK, DV, kLcAll>, (int)Lc<DK, DV>::kSmem, configured[0]);
     if (e != cudaSuccess)
         return e;
     const long long heads = (long long)a.B * a.H, slices = (a.Dv + DV - 1) / DV;
     if (p.nseg > 1) {
-        e = configure_smem(linear_chunked_kernel<DK, DV, true>, (int)Lc<DK, DV>::kSmem, configured[1]);
+        e = configure_smem(linear_chunked_kernel<DK, DV, kLcStates>, (int)Lc<DK, DV>::kSmem, configured[1]);
         if (e != cudaSuccess)
             return e;
-        e = launch_early(linear_chunked_kernel<DK, DV, true>, (unsigned)(heads * (p.nseg - 1) * slices), kLcThreads,
+        e = launch_early(linear_chunked_kernel<DK, DV, kLcStates>, (unsigned)(heads * (p.nseg - 1) * slices), kLcThreads,
                          Lc<DK, DV>::kSmem, s, 1, q, k, v, p);
         if (e != cudaSuccess)
             return e;
     }
-    return launch_early(linear_chunked_kernel<DK, DV, false>, (unsigned)(heads * p.nseg * slices), kLcThreads,
+    if (p.cut) {
+        const int before = (int)(heads * slices) - p.cut;
+        e = launch_early(linear_chunked_kernel<DK, DV, kLcCut>, (unsigned)before, kLcThreads, Lc<DK, DV>::kSmem, s, 1, q, k, v, p);
+        if (e != cudaSuccess)
+            return e;
+        ChunkedArgs rest = p;
+        rest.launched = before;
+        return launch_early(linear_chunked_kernel<DK, DV, kLcCut>, (unsigned)(2 * p.cut), kLcThreads, Lc<DK, DV>::kSmem, s, 1,
+                            q, k, v, rest);
+    }
+    return launch_early(linear_chunked_kernel<DK, DV, kLcAll>, (unsigned)(heads * p.nseg * slices), kLcThreads,
                         Lc<DK, DV>::kSmem, s, 1, q, k, v, p);
 }
 
@@ -853,7 +885,11 @@ int lc_cols(const LinAttnArgs &a) { return a.Dv <= 32 ? 32 : 64; }
 // last one has to add up.  (16 heads of
 // 128 x 128, 2048 tokens, 1 to 4 segments: 36, 37, 31, 28 us;  one head of 128 x 64, 65536 tokens, 8, 16, 36,
 // 72 segments: 212, 124, 92, 105 us.)
-void lc_plan(const LinAttnArgs &a, int *nseg, int *seg_chunks)
+//
+// Where the units fill the last of several waves by half or less, those of that wave are cut in two instead: the first
+// pieces go first, the second ones behind the whole units, when what they start from is long there, and both
+// together fill the SMs.
+void lc_plan(const LinAttnArgs &a, ChunkedArgs *p)
 {
     const long long units = (long long)a.B * a.H * ((a.Dv + lc_cols(a) - 1) / lc_cols(a));
     const int chunks = (a.L + kLcChunk - 1) / kLcChunk;
@@ -864,10 +900,18 @@ void lc_plan(const LinAttnArgs &a, int *nseg, int *seg_chunks)
         const long long cost = (10 * waves + 8 * first) * (each + 3) + (n > 1 ? 20 + 5 * n : 0);
         if (n == 1 || cost < best) {
             best = cost;
-            *seg_chunks = each;
+            p->seg_chunks = each;
         }
     }
-    *nseg = (chunks + *seg_chunks - 1) / *seg_chunks;
+    const int over = (int)(units % kLcSms), half = (chunks + 1) / 2;
+    p->cut = 0;
+    if (units > kLcSms && over > 0 && over <= kLcSms / 2 && chunks > 1 &&
+        10 * (units / kLcSms * (chunks + 3) + half + 3) + 20 < best) {
+        p->cut = over;
+        p->cut_chunks = half;
+        p->seg_chunks = chunks;
+    }
+    p->nseg = (chunks + p->seg_chunks - 1) / p->seg_chunks;
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -876,25 +920,27 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 size_t linear_chunked_workspace(const LinAttnArgs &a)
 {
-    int nseg, seg_chunks;
-    lc_plan(a, &nseg, &seg_chunks);
-    if (nseg == 1)
-        return 0;
+    ChunkedArgs p{};
+    lc_plan(a, &p);
+    if (p.nseg == 1)
+        return (size_t)p.cut * a.Dk * lc_cols(a) * 4;
     const size_t heads = (size_t)a.B * a.H;
-    return round256(heads * nseg * 4) + heads * nseg * a.Dk * a.Dv * 4;
+    return round256(heads * p.nseg * 4) + heads * p.nseg * a.Dk * a.Dv * 4;
 }
 
 cudaError_t launch_linear_chunked(const LinAttnArgs &a, void *workspace, cudaStream_t s)
 {
     ChunkedArgs p{};
     p.a = a;
-    lc_plan(a, &p.nseg, &p.seg_chunks);
+    lc_plan(a, &p);
     const long long heads = (long long)a.B * a.H;
     if (heads * p.nseg * 2 > 0x7fffffffLL || heads * 64 > 0x7fffffffLL)
         return cudaErrorInvalidConfiguration;
     if (p.nseg > 1) {
         p.decays = static_cast<float *>(workspace);
         p.states = reinterpret_cast<float *>(static_cast<char *>(workspace) + round256((size_t)heads * p.nseg * 4));
+    } else if (p.cut) {
+        p.states = static_cast<float *>(workspace);
     }
     if (lc_cols(a) == 32)
         return a.Dk <= 64 ? launch_width<64, 32>(p, s) : launch_width<128, 32>(p, s);

@@ -270,6 +270,33 @@ def test_linear_attention_state_passing_and_in_place():
     _check_attention(q, k, v, gates, scale, state, None, torch.cat(outs, 1), h)
 
 
+@pytest.mark.parametrize("shape", [(20, 700, 2, 8, 64, 64), (40, 900, 1, 2, 24, 72), (19, 1300, 1, 16, 128, 24)])
+def test_linear_attention_cut_units(shape):
+    """A little more than one or two CTAs for each SM, so that the last heads are cut in two: sequences that end
+    in either piece or at the cut, with the state replaced in place; and the same in a graph."""
+    B, L, G, H, Dk, Dv = shape
+    q, k, v, gates, scale, state = _attention_inputs(shape, 18, True, True, True)
+    gates *= 0.1
+    cut = (-(-L // 128) + 1) // 2 * 128
+    lengths = torch.full((B,), L, device="cuda", dtype=torch.int32)
+    lengths[-7:] = torch.tensor([L - 1, cut, cut + 1, cut - 1, 0, 1, L], device="cuda", dtype=torch.int32)
+    ws = torch.full((ss.linear_attention_workspace_size(*shape),), 255, dtype=torch.uint8, device="cuda")
+    assert ws.numel() > 256  # the cut heads' states
+    for n in (None, lengths):
+        h, out = state.clone(), torch.zeros(B, L, H, Dv, device="cuda", dtype=torch.bfloat16)
+        ss.linear_attention(q, k, v, gates, scale=scale, h0=h, h_last=h, lengths=n, out=out, workspace=ws)
+        ss.check_workspace_status(ws)
+        _check_attention(q, k, v, gates, scale, state, n, out, h)
+    again, h2 = torch.zeros_like(out), state.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ss.linear_attention(q, k, v, gates, scale=scale, h0=h2, h_last=h2, lengths=lengths, out=again, workspace=ws)
+    for _ in range(3):
+        h2.copy_(state)
+        graph.replay()
+        assert torch.equal(again, out) and torch.equal(h2, h)
+
+
 @pytest.mark.parametrize("shape", [(1, 700, 1, 2, 128, 96), (2, 300, 1, 2, 64, 40), (1, 8, 1, 2, 16, 40),
                                    (1, 5000, 1, 1, 32, 24)])
 @pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
