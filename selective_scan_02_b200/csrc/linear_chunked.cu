@@ -47,7 +47,7 @@ constexpr int kLcParts = 3;           // of w V
 constexpr int kLcAhead = 3;           // chunks that a tile is asked for in L2 before its load
 constexpr int kLcIdlePolls = 1 << 24;  // of the copy warp, at 120 ns or more: about 2 s
 constexpr int kLcSms = 148;
-constexpr int kLcMaxSegments = 64;
+constexpr int kLcMaxSegments = 149;  // one CTA for each SM in either pass
 
 constexpr float kLcLog2e = 1.4426950408889634f, kLcLn2 = 0.6931471805599453f;
 
@@ -63,9 +63,11 @@ struct alignas(16) ChunkDecay {
 
 struct ChunkedArgs {
     LinAttnArgs a;
-    float *states;       // (B * H, nseg, Dk, Dv): the segments' own states; the last one's place holds h0
-    float *decays;       // (B * H, nseg): the segments' decays
-    int nseg, seg_chunks;
+    // For every segment but the last: (B * H, nseg - 1, Dk, Dv) its own state, then that of the sequence behind it, and
+    // (B * H, nseg - 1) its decay
+    float *states, *decays;
+    int nseg, first_chunks, seg_chunks;  // chunks of the first segment, and of the others
+    int seg_from, segs;                  // the segments of this launch
     // Cut units (a unit: a CTA's columns of one head of one sequence): the last `cut` ones are in two pieces, the first of
     // which leaves its state in `states`.  CTAs take the first pieces, the whole units, then the second pieces.
     int cut, cut_chunks;
@@ -164,37 +166,33 @@ __global__ void __launch_bounds__(kLcThreads, 1)
     int *const marks = reinterpret_cast<int *>(tmem_slot + 2);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
 
-    const int segs = STATES ? p.nseg - 1 : p.nseg;  // the last segment's own state is not carried on
     const int slices = (a.Dv + DV - 1) / DV;
     const int place = (int)blockIdx.x + (CUT ? p.launched : 0), units = a.B * a.H * slices;
     const bool piece0 = CUT && place < p.cut, piece1 = CUT && place >= units;
     const int unit = !CUT ? place : piece0 ? units - p.cut + place : place - p.cut;  // with cut units: one segment
     const int slice = unit % slices;
-    const int seg = unit / slices % segs;
-    const long long bh = unit / slices / segs;
+    const int seg = p.seg_from + unit / slices % p.segs;
+    const long long bh = unit / slices / p.segs;
     const int h = (int)(bh % a.H), b = (int)(bh / a.H);
     const int group = h / (a.H / a.G);
     const int c0 = slice * DV;              // this CTA's columns of v, o and S
     const int cols = min(DV, a.Dv - c0);    // a multiple of 8
-    // Whole units behind the first launch need nothing of it, and all that they read was there before it began.
-    if (!CUT || p.launched == 0 || piece1)
+    // What is launched behind the first launch's start needs nothing of it, but for second pieces (and segments), and all
+    // that it reads was there before that began.
+    if (!STATES && (!CUT || p.launched == 0 || piece1))
         grid_wait();
+    // The launch behind this one waits for this one's end, and means the end of the one before too.
+    const bool holds = STATES && blockIdx.x == gridDim.x - 1;
     const int len = a.lengths ? min(max(a.lengths[b], 0), a.L) : a.L;
-    const int t_first = (piece1 ? p.cut_chunks : seg * p.seg_chunks) * kLcChunk;
-    const int t_end = min(len, t_first + (piece0 ? p.cut_chunks : p.seg_chunks) * kLcChunk);
-    if ((STATES || p.nseg == 1) && place == 0 && threadIdx.x == 0)
+    const int t_first = (piece1 ? p.cut_chunks : seg == 0 ? 0 : p.first_chunks + (seg - 1) * p.seg_chunks) * kLcChunk;
+    const int t_end = min(len, t_first + (piece0 ? p.cut_chunks : seg == 0 ? p.first_chunks : p.seg_chunks) * kLcChunk);
+    if (!STATES && p.seg_from == 0 && place == 0 && threadIdx.x == 0)
         *a.err = 0;  // the call's first kernel, long before any wait of it can run out
-    if (STATES && seg == 0 && a.h0) {
-        // a copy of h0, which the last segment of the pass to come may replace before the others have read it
-        const int per = cols / 4;
-        for (int x = threadIdx.x; x < a.Dk * per; x += kLcThreads) {
-            const long long at = (long long)(x / per) * a.Dv + c0 + x % per * 4;
-            *reinterpret_cast<float4 *>(p.states + (bh * p.nseg + p.nseg - 1) * a.Dk * a.Dv + at) =
-                *reinterpret_cast<const float4 *>(a.h0 + bh * a.Dk * a.Dv + at);
-        }
-    }
-    if (t_first >= len && !(len == 0 && seg == 0 && !piece1 && !STATES))
+    if (t_first >= len && !(len == 0 && seg == 0 && !piece1)) {
+        if (holds)
+            grid_wait();
         return;
+    }
     const int chunks = (t_end - t_first + kLcChunk - 1) / kLcChunk;  // 0 for an empty sequence: its state is kept
 
     if (threadIdx.x == 0) {
@@ -487,7 +485,7 @@ __global__ void __launch_bounds__(kLcThreads, 1)
             arrive(C::kDecFull + dec.slot);
         }
         if (STATES && lane == 0 && good)
-            p.decays[bh * p.nseg + seg] = exp2f((float)whole);
+            p.decays[bh * (p.nseg - 1) + seg] = exp2f((float)whole);
     } else if (warp >= kLcWeight && warp < (STATES ? kLcState : kLcScore)) {
         // V -> w V, 16 bytes at a time.  A part is the upper 16 bits of what the
         // parts before it leave, so the subtractions are exact and three parts hold all 24 bits.
@@ -676,20 +674,11 @@ __global__ void __launch_bounds__(kLcThreads, 1)
                 v[x / 2] = make_float2(f.x, f.y), v[x / 2 + 1] = make_float2(f.z, f.w);
             }
         };
-        load(piece1               ? at_cut
-             : STATES || !a.h0 ? nullptr
-                               : (p.nseg > 1 ? p.states + (bh * p.nseg + p.nseg - 1) * size : a.h0 + bh * size) + in_head,
+        load(piece1    ? at_cut
+             : seg > 0 ? (STATES ? nullptr : p.states + (bh * (p.nseg - 1) + seg - 1) * size + in_head)
+             : a.h0    ? a.h0 + bh * size + in_head
+                       : nullptr,
              s);
-        // the state before this segment, from the segments before it
-        if (!STATES)
-            for (int i = 0; i < seg; ++i) {
-                float2 own[kMine / 2];
-                load(p.states + (bh * p.nseg + i) * size + in_head, own);
-                const float d = p.decays[bh * p.nseg + i];
-#pragma unroll
-                for (int x = 0; x < kMine / 2; ++x)
-                    s[x] = __ffma2_rn(s[x], make_float2(d, d), own[x]);
-            }
         // the bf16 copy of S, its 16-byte pieces swizzled as TMA would
         auto publish = [&] {
             if (row < DK) {
@@ -753,9 +742,9 @@ __global__ void __launch_bounds__(kLcThreads, 1)
 #pragma unroll
             for (int x = 0; x < kMine; x += 4)
                 *reinterpret_cast<float4 *>(at_cut + x) = make_float4(s[x / 2].x, s[x / 2].y, s[x / 2 + 1].x, s[x / 2 + 1].y);
-        float *const to = STATES                     ? p.states + (bh * p.nseg + seg) * size + in_head
-                          : a.h_last && t_end == len ? a.h_last + bh * size + in_head
-                                                     : nullptr;
+        float *const to = !STATES && t_end == len       ? (a.h_last ? a.h_last + bh * size + in_head : nullptr)
+                          : STATES || (seg == 0 && p.nseg > 1) ? p.states + (bh * (p.nseg - 1) + seg) * size + in_head
+                                                                 : nullptr;
         if (good && to && mine)
 #pragma unroll
             for (int x = 0; x < kMine; x += 4)
@@ -825,6 +814,41 @@ __global__ void __launch_bounds__(kLcThreads, 1)
     __syncthreads();
     if (warp == 1)
         tc::tmem_free(tmem, 512);
+    if (holds)
+        grid_wait();
+}
+
+// The segments' own states -> the state behind each: one thread for four elements of a head's state, with the
+// loads of kLcCarry segments on their way at once.
+constexpr int kLcCarry = 8, kLcCarryThreads = 128;
+
+__global__ void __launch_bounds__(kLcCarryThreads) linear_carry_kernel(float *states, const float *decays, int segs, int size4,
+                                                                       long long total)
+{
+    grid_next();
+    grid_wait();
+    const long long e = (long long)blockIdx.x * kLcCarryThreads + threadIdx.x;
+    if (e >= total)
+        return;
+    const long long head = e / size4;
+    float4 *const at = reinterpret_cast<float4 *>(states) + head * segs * size4 + e % size4;
+    const float *const d = decays + head * segs;
+    float4 s = at[0];
+    for (int i0 = 1; i0 < segs; i0 += kLcCarry) {
+        float4 own[kLcCarry];
+        float by[kLcCarry];
+#pragma unroll
+        for (int i = 0; i < kLcCarry; ++i)
+            if (i0 + i < segs)
+                own[i] = at[(long long)(i0 + i) * size4], by[i] = d[i0 + i];
+#pragma unroll
+        for (int i = 0; i < kLcCarry; ++i)
+            if (i0 + i < segs) {
+                s = make_float4(fmaf(s.x, by[i], own[i].x), fmaf(s.y, by[i], own[i].y), fmaf(s.z, by[i], own[i].z),
+                                fmaf(s.w, by[i], own[i].w));
+                at[(long long)(i0 + i) * size4] = s;
+            }
+    }
 }
 
 // Tensor map over (batch, token, head, column), boxes of 128 tokens by 64 columns of one head.
@@ -853,38 +877,47 @@ cudaError_t launch_width(const ChunkedArgs &p, cudaStream_t s)
                   : configure_smem(linear_chunked_kernel<DK, DV, kLcAll>, (int)Lc<DK, DV>::kSmem, configured[0]);
     if (e != cudaSuccess)
         return e;
-    const long long heads = (long long)a.B * a.H, slices = (a.Dv + DV - 1) / DV;
-    if (p.nseg > 1) {
-        e = configure_smem(linear_chunked_kernel<DK, DV, kLcStates>, (int)Lc<DK, DV>::kSmem, configured[1]);
-        if (e != cudaSuccess)
-            return e;
-        e = launch_early(linear_chunked_kernel<DK, DV, kLcStates>, (unsigned)(heads * (p.nseg - 1) * slices), kLcThreads,
-                         Lc<DK, DV>::kSmem, s, 1, q, k, v, p);
-        if (e != cudaSuccess)
-            return e;
-    }
+    const unsigned units = (unsigned)((long long)a.B * a.H * ((a.Dv + DV - 1) / DV));
+    ChunkedArgs part = p;
+    part.segs = 1;
     if (p.cut) {
-        const int before = (int)(heads * slices) - p.cut;
-        e = launch_early(linear_chunked_kernel<DK, DV, kLcCut>, (unsigned)before, kLcThreads, Lc<DK, DV>::kSmem, s, 1, q, k, v, p);
+        const unsigned before = units - p.cut;
+        e = launch_early(linear_chunked_kernel<DK, DV, kLcCut>, before, kLcThreads, Lc<DK, DV>::kSmem, s, 1, q, k, v, part);
         if (e != cudaSuccess)
             return e;
-        ChunkedArgs rest = p;
-        rest.launched = before;
-        return launch_early(linear_chunked_kernel<DK, DV, kLcCut>, (unsigned)(2 * p.cut), kLcThreads, Lc<DK, DV>::kSmem, s, 1,
-                            q, k, v, rest);
+        part.launched = (int)before;
+        return launch_early(linear_chunked_kernel<DK, DV, kLcCut>, 2u * p.cut, kLcThreads, Lc<DK, DV>::kSmem, s, 1, q, k, v, part);
     }
-    return launch_early(linear_chunked_kernel<DK, DV, kLcAll>, (unsigned)(heads * p.nseg * slices), kLcThreads,
-                        Lc<DK, DV>::kSmem, s, 1, q, k, v, p);
+    e = launch_early(linear_chunked_kernel<DK, DV, kLcAll>, units, kLcThreads, Lc<DK, DV>::kSmem, s, 1, q, k, v, part);
+    if (e != cudaSuccess || p.nseg == 1)
+        return e;
+    part.seg_from = 1;
+    if (p.nseg > 2) {
+        part.segs = p.nseg - 2;
+        e = configure_smem(linear_chunked_kernel<DK, DV, kLcStates>, (int)Lc<DK, DV>::kSmem, configured[1]);
+        if (e == cudaSuccess)
+            e = launch_early(linear_chunked_kernel<DK, DV, kLcStates>, units * part.segs, kLcThreads, Lc<DK, DV>::kSmem, s, 1,
+                             q, k, v, part);
+        const long long elements = (long long)a.B * a.H * a.Dk * a.Dv / 4;
+        if (e == cudaSuccess)
+            e = launch_early(linear_carry_kernel, (unsigned)((elements + kLcCarryThreads - 1) / kLcCarryThreads), kLcCarryThreads,
+                             0, s, 1, p.states, (const float *)p.decays, p.nseg - 1, a.Dk * a.Dv / 4, elements);
+        if (e != cudaSuccess)
+            return e;
+    }
+    part.segs = p.nseg - 1;
+    return launch_early(linear_chunked_kernel<DK, DV, kLcAll>, units * part.segs, kLcThreads, Lc<DK, DV>::kSmem, s, 1, q, k, v,
+                        part);
 }
 
 // Columns of the state in one CTA.
 int lc_cols(const LinAttnArgs &a) { return a.Dv <= 32 ? 32 : 64; }
 
-// Segments of a sequence, by the time they take in chunks: both passes' waves of CTAs, with three chunks to fill and
-// drain a CTA (the first pass takes 0.8 of the second's time), and half a chunk for each segment's state that the
-// last one has to add up.  (16 heads of
-// 128 x 128, 2048 tokens, 1 to 4 segments: 36, 37, 31, 28 us;  one head of 128 x 64, 65536 tokens, 8, 16, 36,
-// 72 segments: 212, 124, 92, 105 us.)
+// Segments of a sequence, and cut units, by the time that they take in tenths of a chunk's: whole waves of CTAs, two
+// or three chunks to fill and drain a CTA, 0.55 of a chunk's time for one of the first pass (the first segment, which
+// needs no such pass, is shorter than the others so as to end with theirs), and what the launches and the sums between
+// the passes take.  (us for 16 heads of 128 x 128: 2048 tokens, 1, 3, 4 segments: 38, 39, 35;  32768 tokens, 4, 5,
+// 9, 10: 247, 212, 230, 244.  One head of 128 x 64, 65536 tokens, 24, 48, 75, 103: 83, 53, 44, 41.)
 //
 // Where the units fill the last of several waves by half or less, those of that wave are cut in two instead: the first
 // pieces go first, the second ones behind the whole units, when what they start from is long there, and both
@@ -893,25 +926,29 @@ void lc_plan(const LinAttnArgs &a, ChunkedArgs *p)
 {
     const long long units = (long long)a.B * a.H * ((a.Dv + lc_cols(a) - 1) / lc_cols(a));
     const int chunks = (a.L + kLcChunk - 1) / kLcChunk;
-    long long best = 0;
-    for (int n = 1; n <= kLcMaxSegments && n <= chunks; ++n) {
-        const int each = (chunks + n - 1) / n;
-        const long long waves = (units * n + kLcSms - 1) / kLcSms, first = (units * (n - 1) + kLcSms - 1) / kLcSms;
-        const long long cost = (10 * waves + 8 * first) * (each + 3) + (n > 1 ? 20 + 5 * n : 0);
-        if (n == 1 || cost < best) {
+    long long best = 10 * ((units + kLcSms - 1) / kLcSms) * (chunks + 2);
+    p->nseg = 1, p->cut = 0;
+    p->first_chunks = p->seg_chunks = chunks;
+    for (int n = 3; n <= kLcMaxSegments && n <= chunks; ++n) {
+        const int each = (int)((100LL * chunks + 100 * n - 46) / (100 * n - 45));  // of n - 1 segments and 0.55 of one
+        const int rest = (chunks - 1) / each, first = chunks - rest * each;       // at least one chunk
+        const long long waves = (units * rest + kLcSms - 1) / kLcSms;
+        const long long cost = waves * (5 * max(each, 2 * first) + 10 * each + 45) + 30 + n / 2;
+        if (rest > 1 && cost < best) {
             best = cost;
+            p->nseg = rest + 1;
+            p->first_chunks = first;
             p->seg_chunks = each;
         }
     }
     const int over = (int)(units % kLcSms), half = (chunks + 1) / 2;
-    p->cut = 0;
     if (units > kLcSms && over > 0 && over <= kLcSms / 2 && chunks > 1 &&
-        10 * (units / kLcSms * (chunks + 3) + half + 3) + 20 < best) {
+        10 * (units / kLcSms * (chunks + 2) + half + 2) + 20 < best) {
+        p->nseg = 1;
         p->cut = over;
         p->cut_chunks = half;
-        p->seg_chunks = chunks;
+        p->first_chunks = p->seg_chunks = chunks;
     }
-    p->nseg = (chunks + p->seg_chunks - 1) / p->seg_chunks;
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -925,7 +962,7 @@ size_t linear_chunked_workspace(const LinAttnArgs &a)
     if (p.nseg == 1)
         return (size_t)p.cut * a.Dk * lc_cols(a) * 4;
     const size_t heads = (size_t)a.B * a.H;
-    return round256(heads * p.nseg * 4) + heads * p.nseg * a.Dk * a.Dv * 4;
+    return round256(heads * (p.nseg - 1) * 4) + heads * (p.nseg - 1) * a.Dk * a.Dv * 4;
 }
 
 cudaError_t launch_linear_chunked(const LinAttnArgs &a, void *workspace, cudaStream_t s)
@@ -938,7 +975,7 @@ cudaError_t launch_linear_chunked(const LinAttnArgs &a, void *workspace, cudaStr
         return cudaErrorInvalidConfiguration;
     if (p.nseg > 1) {
         p.decays = static_cast<float *>(workspace);
-        p.states = reinterpret_cast<float *>(static_cast<char *>(workspace) + round256((size_t)heads * p.nseg * 4));
+        p.states = reinterpret_cast<float *>(static_cast<char *>(workspace) + round256((size_t)heads * (p.nseg - 1) * 4));
     } else if (p.cut) {
         p.states = static_cast<float *>(workspace);
     }

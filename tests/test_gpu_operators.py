@@ -331,15 +331,15 @@ def test_linear_attention_not_finite(shape, value):
     assert not out[hit].isfinite().any() and torch.equal(out[~hit], clean[~hit]) and torch.equal(last, clean_last)
 
 
-def test_linear_attention_segments_ragged_and_in_place():
+@pytest.mark.parametrize("shape", [(4, 4000, 1, 1, 128, 96), (4, 9000, 1, 1, 24, 40)])
+def test_linear_attention_segments_ragged_and_in_place(shape):
     """Few heads, so that a sequence is cut into segments: lengths that end in the first, an inner and the last
     one, or before the first token, with the state replaced in place."""
-    shape = (4, 4000, 1, 1, 128, 96)
     B, L, G, H, Dk, Dv = shape
     q, k, v, gates, scale, state = _attention_inputs(shape, 16, True, True, True)
     gates[:, 2000:2050:7] = -math.inf
     gates *= 0.02  # slow: what the segments carry counts
-    lengths = torch.tensor([4000, 2500, 0, 131], device="cuda", dtype=torch.int32)
+    lengths = torch.tensor([L, 2500, 0, 131], device="cuda", dtype=torch.int32)
     out = torch.zeros(B, L, H, Dv, device="cuda", dtype=torch.bfloat16)
     h = state.clone()
     ss.linear_attention(q, k, v, gates, scale=scale, h0=h, h_last=h, lengths=lengths, out=out)
