@@ -270,7 +270,8 @@ def test_linear_attention_state_passing_and_in_place():
     _check_attention(q, k, v, gates, scale, state, None, torch.cat(outs, 1), h)
 
 
-@pytest.mark.parametrize("shape", [(20, 700, 2, 8, 64, 64), (40, 900, 1, 2, 24, 72), (19, 1300, 1, 16, 128, 24)])
+@pytest.mark.parametrize("shape", [(20, 700, 2, 8, 64, 64), (40, 900, 1, 2, 24, 72), (19, 1300, 1, 16, 128, 24),
+                                   (32, 650, 1, 5, 16, 16)])
 def test_linear_attention_cut_units(shape):
     """A little more than one or two CTAs for each SM, so that the last heads are cut in two: sequences that end
     in either piece or at the cut, with the state replaced in place; and the same in a graph."""
