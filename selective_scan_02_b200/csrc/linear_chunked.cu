@@ -29,8 +29,16 @@
 // factor, both at most 1; only the diagonal blocks need an exponential for each element.
 //
 // Where the heads of all sequences are too few for the GPU, a sequence is cut into segments: a first
-// pass sums each segment's own state (K and V only), and the pass above starts each segment from the sum of
-// those before it, each decayed by what lies between.
+// pass sums each segment's own state (K and V only), a small kernel adds them up along the sequence, each decayed by
+// what lies between, and the pass above starts each segment from the state before it.  The first segment needs no first
+// pass: it goes beside the others' ones.
+//
+// What bounds it: a chunk of 128 x 64 columns takes about 3700 cycles.  Shared memory passes 2950 cycles' worth of bytes
+// in them (tiles in, w V out, and the MMAs' operands: 64 columns read all of Q and K), the warps issue 0.6 instructions a
+// cycle and scheduler, the tensor cores are busy 40 %, and hand-overs between the warps (load, scores, P, P V, output;
+// K^T w V, state, Q S) fill the rest.  32768 tokens of 16 heads of 128 x 128: 214 us, of which the first pass
+// is 68 (floor 82 us, bytes); 32 x 3136 tokens of 6 heads of 64 x 32: 58 us (floor 16).  Without its arithmetic, barriers
+// and MMAs alone, the kernel takes three quarters of its time.
 #include "api_internal.h"
 #include "launch_util.h"
 #include "linear_attention.h"
