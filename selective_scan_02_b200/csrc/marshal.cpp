@@ -4,6 +4,7 @@
 // The operators serve single tokens, where a call's time on the GPU is a few microseconds; the same checks and
 // allocations made from Python take three times as long as the call.  Everything runs on the current stream of
 // the tensors' device, which need not be the current device.
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -82,7 +83,7 @@ struct Call {
 
     at::Tensor make(c10::IntArrayRef shape, at::ScalarType type) const
     {
-        return at::empty(shape, at::TensorOptions().dtype(type).device(device));
+        return at::Tensor(at::detail::empty_cuda(shape, type, device, std::nullopt));
     }
     void check(const at::Tensor &t, const char *name, at::ScalarType type, c10::IntArrayRef shape) const
     {
