@@ -9,8 +9,10 @@
 // head's state in registers: 8 lanes of 4 columns (16-byte accesses, a 128-byte run for each
 // row of the state) by 16 rows at a time, so that even one sequence of few heads spreads over
 // many SMs, and all of the state's loads are in flight at once.  Columns of the state do not
-// meet: o's column j needs column j of S alone.  64 rows of 32 heads of 128 x 128 (270 MB): 45 to 47 us, 5.7 to
-// 6.0 TB/s; one row of 16 heads: 3.4 us a call, what launching it takes.
+// meet: o's column j needs column j of S alone.  The state is not
+// wanted again before the other layers' states have passed, so its accesses are marked as streaming: 64 rows of 32
+// heads of 128 x 128 (270 MB) 46.4 -> 43.0 us, 6.3 TB/s, and no slower where it all fits L2 (24 heads of 64 x 96,
+// 33 rows: 9.1 us both).  One row of 16 heads: 3.4 us a call, what launching it takes.  64 columns a CTA: 48.7 us.
 #include "launch_util.h"
 #include "linear_attention.h"
 
@@ -77,7 +79,7 @@ __global__ void __launch_bounds__(kLrThreads) linear_recurrent_kernel(const LinA
         const int r = r0 + i * kLrGroups;
         s[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (a.h0 && cols && r < a.Dk)
-            s[i] = *reinterpret_cast<const float4 *>(a.h0 + at + (size_t)r * a.Dv + c);
+            s[i] = __ldcs(reinterpret_cast<const float4 *>(a.h0 + at + (size_t)r * a.Dv + c));
     }
 
     // the first row of this slot after `from`; a.B if there is none
@@ -172,7 +174,7 @@ __global__ void __launch_bounds__(kLrThreads) linear_recurrent_kernel(const LinA
         for (int i = 0; i < kLrRows; ++i) {
             const int r = r0 + i * kLrGroups;
             if (r < a.Dk)
-                *reinterpret_cast<float4 *>(a.h_last + at + (size_t)r * a.Dv + c) = s[i];
+                __stcs(reinterpret_cast<float4 *>(a.h_last + at + (size_t)r * a.Dv + c), s[i]);
         }
     }
 }
