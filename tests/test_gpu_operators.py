@@ -598,6 +598,36 @@ def test_layer_in_a_graph_on_two_streams():
                 assert torch.equal(got, want)
 
 
+def test_calls_on_several_streams_at_once():
+    """Calls in flight together, of every kind of split: cut heads, segments, clusters, and the step."""
+    calls, wanted = [], []
+    for i, shape in enumerate([(20, 700, 2, 8, 64, 64), (1, 9000, 1, 2, 128, 96), (3, 500, 1, 2, 40, 24)]):
+        q, k, v, gates, scale, state = _attention_inputs(shape, 70 + i, True, True, True)
+        calls.append(lambda q=q, k=k, v=v, g=gates, s=state: ss.linear_attention(q, k, v, g, h0=s, return_last_state=True))
+    for i, (m, n, k) in enumerate([(4, 4096, 2048), (100, 512, 4096), (700, 900, 1040)]):
+        a, sa, w, sw, bias = _matmul_inputs(m, n, k, 80 + i)
+        calls.append(lambda a=a, sa=sa, w=w, sw=sw, b=bias: (ss.matmul_fp8(a, sa, w, sw, bias=b),))
+    q, k, v, gates, scale, state = _attention_inputs((30, 1, 4, 8, 128, 64), 90, True, True, False, lead=(30,))
+
+    def step():
+        s = state.clone()
+        return ss.linear_attention_step(q, k, v, gates, s), s
+
+    calls.append(step)
+    wanted = [[t.clone() for t in call()] for call in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(5):
+        got = []
+        for s, call in zip(streams, calls):
+            with torch.cuda.stream(s):
+                got.append(call())
+                got[-1] = call()
+        torch.cuda.synchronize()
+        for have, want in zip(got, wanted):
+            assert all(torch.equal(x, y) for x, y in zip(have, want))
+
+
 def test_layer_on_a_given_stream():
     layer, d = _Layer(), 256
     x = torch.randn(2, 40, d, device="cuda", generator=_gen(34)).bfloat16()
