@@ -86,6 +86,19 @@ def test_rms_norm_many_rows():
     _check_norm(x, w, None, "bf16", ss.rms_norm(x, w, eps=1e-6), 1e-6)
 
 
+@pytest.mark.parametrize("d", [264, 333, 384, 512, 640, 701, 1000, 1301, 1536, 2048, 2049, 2560, 4096, 5001, 5120, 8192, 10000, 12285,
+                               16384, 20000, 20001, 24576, 32768])
+def test_rms_norm_widths_of_many_rows(d):
+    """A row more than two for each SM: other splits of a row than the few rows' above."""
+    g = _gen(d)
+    x = torch.randn(297, d, device="cuda", generator=g).bfloat16()
+    w = 1 + 0.3 * torch.randn(d, device="cuda", generator=g)
+    for out, res in (("e4m3", torch.randn(297, d, device="cuda", generator=g)), ("bf16", None),
+                     ("f32", torch.randn(297, d, device="cuda", generator=g).bfloat16())):
+        _check_norm(x, w, res, out, ss.rms_norm(x, w, residual=res, eps=1e-5, out_dtype=TYPES[out]), 1e-5)
+        _check_norm(x.float(), w, res, out, ss.rms_norm(x.float(), w, residual=res, eps=1e-5, out_dtype=TYPES[out]), 1e-5)
+
+
 def test_rms_norm_in_place_and_leading_dimensions():
     g = _gen(5)
     x = torch.randn(2, 3, 320, device="cuda", generator=g).bfloat16()
