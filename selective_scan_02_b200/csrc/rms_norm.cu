@@ -126,9 +126,9 @@ __device__ __forceinline__ float rn_scale(float amax)
 
 // TPR threads hold a row, each 8 NV of its columns.
 //   VEC (D % 8 == 0, rows 16-byte aligned): NV runs of 8 neighbouring columns, run t + i * TPR of thread
-//   t; a group of 128 columns is one run of 16 neighbouring lanes.
-//   else (TPR a multiple of 32): single columns, a warp's 256 NV next to one another and 32 of them in
-//   the lanes, so that accesses of rows of any alignment stay together; a group is four of a warp's 32.
+//   t; a group of 128 columns is one run of 16 neighbouring lanes (or all of fewer).
+//   else: single columns, a warp's 256 NV (or the row's) next to one another and 32 of them (or TPR) in the
+//   lanes, so that accesses of rows of any alignment stay together; a group is four of a warp's 32, or eight of 16.
 // The types of x and the residual are the template's, so that all of a thread's loads are issued before
 // the first is used.  y is (r weight) rstd, and q is (r weight) (rstd / s): with the arithmetic in pairs
 // (f32x2) a column takes about eight instructions, which the loads hide.
@@ -145,7 +145,9 @@ __global__ void __launch_bounds__(TPR > kRnThreads ? TPR : kRnThreads) rms_norm_
     const long long row = (long long)blockIdx.x * kRows + threadIdx.x / TPR;
     const bool live = row < a.rows;
     const long long at = row * a.D;
-    const int first = t / 32 * (256 * NV) + t % 32;  // (single columns)
+    constexpr int kStep = TPR < 32 ? TPR : 32;             // single columns: in the lanes,
+    constexpr int kPer = kStep == 32 ? 4 : 8;              // and of a group in one of them
+    const int first = t / 32 * (256 * NV) + t % kStep;
     const bool e4m3 = a.y_dtype == SS2D_E4M3;
     grid_wait();
     grid_next();
@@ -187,7 +189,7 @@ __global__ void __launch_bounds__(TPR > kRnThreads ? TPR : kRnThreads) rms_norm_
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int c = first + (8 * i + j) * 32;
+                const int c = first + (8 * i + j) * kStep;
                 const bool in = live && c < a.D;
                 f[i][j] = in ? rn_load<XBF16>(a.x, at + c) : 0.0f;
                 if (RES)
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(TPR > kRnThreads ? TPR : kRnThreads) rms_norm_
             if (RES)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const int c = first + (8 * i + j) * 32;
+                    const int c = first + (8 * i + j) * kStep;
                     f[i][j] += e[i][j];
                     if (live && c < a.D)
                         rn_store(a.residual_out, kResType, at + c, f[i][j]);
@@ -245,7 +247,7 @@ __global__ void __launch_bounds__(TPR > kRnThreads ? TPR : kRnThreads) rms_norm_
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     amax = fmaxf(amax, fmaxf(fabsf(r[i][j].x), fabsf(r[i][j].y)));
-                const float s = rn_scale<16>(amax * rstd);
+                const float s = rn_scale<TPR < 16 ? TPR : 16>(amax * rstd);
                 k = __fdividef(rstd, s);
                 if (in && c % kRnGroup == 0)
                     a.scales[row * a.groups + c / kRnGroup] = s;
@@ -257,26 +259,27 @@ __global__ void __launch_bounds__(TPR > kRnThreads ? TPR : kRnThreads) rms_norm_
                 rn_store8(a.y, a.y_dtype, at + c, r[i]);
         } else {
 #pragma unroll
-            for (int h = 0; h < 4; h += 2) {
-                const int c = first + (8 * i + 2 * h) * 32;  // this lane's column in the group's first 32
-                float f[4] = {r[i][h].x, r[i][h].y, r[i][h + 1].x, r[i][h + 1].y};
+            for (int h = 0; h < 8; h += kPer) {
+                const int c = first + (8 * i + h) * kStep;  // this lane's first column in the group
+                float f[kPer];
                 float amax = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    f[j] = c + j * 32 < a.D ? f[j] * __ldg(a.weight + c + j * 32) : 0.0f;
+                for (int j = 0; j < kPer; ++j) {
+                    const float2 pair = r[i][(h + j) / 2];
+                    f[j] = c + j * kStep < a.D ? (j % 2 ? pair.y : pair.x) * __ldg(a.weight + c + j * kStep) : 0.0f;
                     amax = fmaxf(amax, fabsf(f[j]));
                 }
                 float k = rstd;
                 if (e4m3) {
-                    const float s = rn_scale<32>(amax * rstd);
+                    const float s = rn_scale<kStep>(amax * rstd);
                     k = __fdividef(rstd, s);
-                    if (live && t % 32 == 0 && c < a.D)
+                    if (live && t % kStep == 0 && c < a.D)
                         a.scales[row * a.groups + c / kRnGroup] = s;
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (live && c + j * 32 < a.D)
-                        rn_store(a.y, a.y_dtype, at + c + j * 32, f[j] * k);
+                for (int j = 0; j < kPer; ++j)
+                    if (live && c + j * kStep < a.D)
+                        rn_store(a.y, a.y_dtype, at + c + j * kStep, f[j] * k);
             }
         }
     }
@@ -296,10 +299,9 @@ cudaError_t rms_launch_types(const RmsArgs &a, cudaStream_t s)
 template <int TPR, int NV>
 cudaError_t rms_launch(const RmsArgs &a, cudaStream_t s)
 {
-    constexpr int kWide = TPR < 32 ? 32 : TPR;  // single columns need whole warps
     if (a.D % 8 == 0)
         return a.x_bf16 ? rms_launch_types<TPR, NV, true, true>(a, s) : rms_launch_types<TPR, NV, true, false>(a, s);
-    return a.x_bf16 ? rms_launch_types<kWide, NV, false, true>(a, s) : rms_launch_types<kWide, NV, false, false>(a, s);
+    return a.x_bf16 ? rms_launch_types<TPR, NV, false, true>(a, s) : rms_launch_types<TPR, NV, false, false>(a, s);
 }
 
 size_t rms_esize(int dtype) { return dtype == SS2D_F32 ? 4 : dtype == SS2D_BF16 ? 2 : 1; }
@@ -365,10 +367,19 @@ extern "C" int ss2d_rms_norm(const void *x, int x_dtype, const void *residual, i
     // Many rows: 16 or 24 columns a thread, whichever fits the row better, so that each has several loads in flight, a
     // row needs few warps and few threads have no column.  (2^25 elements, bf16 with a bf16 residual to e4m3: 5120 columns
     // 43 us in 256 threads of 24, 55 in 512 of 16;  24576 columns 45 us in 1024 of 24, 73 in 1024 of 32.)  Few rows (less
-    // than two for each SM): 8 columns a thread, the shortest way through a row.
+    // than two for each SM): 8 columns a thread, the shortest way through a row.  Narrow rows: as many lanes as they need
+    // (100352 rows of 7, 33, 100 columns: 33 us with a warp for each row, 4, 10, 18 so).
     const bool many = rows > 2 * 148;
     cudaError_t e;
-    if (D <= 128)
+    if (D <= 8)
+        e = rms_launch<1, 1>(a, s);
+    else if (D <= 16)
+        e = rms_launch<2, 1>(a, s);
+    else if (D <= 32)
+        e = rms_launch<4, 1>(a, s);
+    else if (D <= 64)
+        e = rms_launch<8, 1>(a, s);
+    else if (D <= 128)
         e = rms_launch<16, 1>(a, s);
     else if (D <= 256)
         e = rms_launch<32, 1>(a, s);
@@ -376,7 +387,7 @@ extern "C" int ss2d_rms_norm(const void *x, int x_dtype, const void *residual, i
         e = rms_launch<256, 1>(a, s);
     else if (!many && D <= 8192)
         e = rms_launch<1024, 1>(a, s);
-    else if (D <= 16 * 24 && D % 8 == 0)  // (single columns need a whole warp)
+    else if (D <= 16 * 24 && D % 8 == 0)  // (333 columns: 79 us so, 76 below)
         e = rms_launch<16, 3>(a, s);
     else if (D <= 32 * 16)
         e = rms_launch<32, 2>(a, s);

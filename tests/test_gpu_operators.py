@@ -86,8 +86,9 @@ def test_rms_norm_many_rows():
     _check_norm(x, w, None, "bf16", ss.rms_norm(x, w, eps=1e-6), 1e-6)
 
 
-@pytest.mark.parametrize("d", [264, 333, 384, 512, 640, 701, 1000, 1301, 1536, 2048, 2049, 2560, 4096, 5001, 5120, 8192, 10000, 12285,
-                               16384, 20000, 20001, 24576, 32768])
+@pytest.mark.parametrize("d", [1, 2, 7, 8, 9, 16, 17, 24, 31, 33, 40, 64, 65, 100, 128, 129, 201, 264, 333, 384,
+                               512, 640, 701, 1000, 1301, 1536, 2048, 2049, 2560, 4096, 5001, 5120, 8192, 10000, 12285, 16384,
+                               20000, 20001, 24576, 32768])
 def test_rms_norm_widths_of_many_rows(d):
     """A row more than two for each SM: other splits of a row than the few rows' above."""
     g = _gen(d)
