@@ -22,12 +22,14 @@ namespace {
 constexpr int kLrThreads = 128;
 constexpr int kLrCols = 32;                       // columns of the state in one CTA
 constexpr int kLrGroups = kLrThreads / (kLrCols / 4);  // rows of the state held by the CTA at a time
-constexpr int kLrRows = kLaMaxDim / kLrGroups;    // rows of the state held by one thread
 
 // STEP: the tokens of this CTA are the rows of the batch that name its slot, in their order (one,
 // where no slot is named twice; the CTAs of the later ones have nothing to do).  Otherwise they
 // are the tokens of sequence b.
-template <bool STEP>
+//
+// ROWS: of the state held by one thread; Dk at most kLrGroups times as many.  (128 rows of 32 heads of 64 x 64: 19.5 us
+// with four, 24.5 with the eight that Dk = 128 needs.)
+template <bool STEP, int ROWS>
 __global__ void __launch_bounds__(kLrThreads) linear_recurrent_kernel(const LinAttnArgs a)
 {
     __shared__ float sq[kLaMaxDim], sk[kLaMaxDim];
@@ -73,9 +75,9 @@ __global__ void __launch_bounds__(kLrThreads) linear_recurrent_kernel(const LinA
     }
 
     const size_t at = ((size_t)slot * a.H + h) * (size_t)a.Dk * a.Dv;
-    float4 s[kLrRows];
+    float4 s[ROWS];
 #pragma unroll
-    for (int i = 0; i < kLrRows; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
         const int r = r0 + i * kLrGroups;
         s[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (a.h0 && cols && r < a.Dk)
@@ -123,7 +125,7 @@ __global__ void __launch_bounds__(kLrThreads) linear_recurrent_kernel(const LinA
         __syncthreads();
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int i = 0; i < kLrRows; ++i) {
+        for (int i = 0; i < ROWS; ++i) {
             const int r = r0 + i * kLrGroups;
             if (r < a.Dk) {
                 const float kr = sk[r], qr = sq[r];
@@ -171,12 +173,20 @@ __global__ void __launch_bounds__(kLrThreads) linear_recurrent_kernel(const LinA
     }
     if (a.h_last && cols) {
 #pragma unroll
-        for (int i = 0; i < kLrRows; ++i) {
+        for (int i = 0; i < ROWS; ++i) {
             const int r = r0 + i * kLrGroups;
             if (r < a.Dk)
                 __stcs(reinterpret_cast<float4 *>(a.h_last + at + (size_t)r * a.Dv + c), s[i]);
         }
     }
+}
+
+template <bool STEP>
+cudaError_t launch_rows(const LinAttnArgs &a, int rows, unsigned grid, cudaStream_t s)
+{
+    return rows <= 2   ? launch_early(linear_recurrent_kernel<STEP, 2>, grid, kLrThreads, 0, s, 1, a)
+           : rows <= 4 ? launch_early(linear_recurrent_kernel<STEP, 4>, grid, kLrThreads, 0, s, 1, a)
+                       : launch_early(linear_recurrent_kernel<STEP, kLaMaxDim / kLrGroups>, grid, kLrThreads, 0, s, 1, a);
 }
 
 }  // namespace
@@ -186,8 +196,8 @@ cudaError_t launch_linear_recurrent(const LinAttnArgs &a, bool step, cudaStream_
     const long long grid = (long long)a.B * a.H * ((a.Dv + kLrCols - 1) / kLrCols);
     if (grid > 0x7fffffffLL)
         return cudaErrorInvalidConfiguration;
-    return step ? launch_early(linear_recurrent_kernel<true>, (unsigned)grid, kLrThreads, 0, s, 1, a)
-                : launch_early(linear_recurrent_kernel<false>, (unsigned)grid, kLrThreads, 0, s, 1, a);
+    const int rows = (a.Dk + kLrGroups - 1) / kLrGroups;
+    return step ? launch_rows<true>(a, rows, (unsigned)grid, s) : launch_rows<false>(a, rows, (unsigned)grid, s);
 }
 
 }  // namespace ss2d

@@ -27,6 +27,16 @@ void wr(const std::string &f, const std::vector<T> &v)
     fwrite(v.data(), sizeof(T), v.size(), fo);
     fclose(fo);
 }
+template <bool STEP>
+void run(const LinAttnArgs &a, unsigned grid)
+{
+    const int rows = (a.Dk + kLrGroups - 1) / kLrGroups;
+    emu_grid(grid, 1, kLrThreads, kEmuShared, [&] {
+        if (rows <= 2) linear_recurrent_kernel<STEP, 2>(a);
+        else if (rows <= 4) linear_recurrent_kernel<STEP, 4>(a);
+        else linear_recurrent_kernel<STEP, kLaMaxDim / kLrGroups>(a);
+    });
+}
 int main(int argc, char **argv)
 {
     if (argc < 11) return 1;
@@ -59,15 +69,14 @@ int main(int argc, char **argv)
     a.scale = 0.5f, a.per_token = per_token;
     a.B = B, a.L = L, a.G = G, a.H = H, a.Dk = Dk, a.Dv = Dv, a.pool = pool;
     const unsigned grid = (unsigned)(B * H * ((Dv + kLrCols - 1) / kLrCols));
-    const size_t smem = kEmuShared;
     if (mode < 2) {
         a.lengths = mode == 1 ? rows.data() : nullptr;
         a.err = &err;
-        emu_grid(grid, 1, kLrThreads, smem, [&] { linear_recurrent_kernel<false>(a); });
+        run<false>(a, grid);
         if (err != 0) { fprintf(stderr, "error word %d\n", err); return 3; }
     } else {
         a.slots = mode == 3 ? rows.data() : nullptr;
-        emu_grid(grid, 1, kLrThreads, smem, [&] { linear_recurrent_kernel<true>(a); });
+        run<true>(a, grid);
     }
     wr(dir + "/out", out);
     wr(dir + "/state", state);

@@ -55,7 +55,7 @@ def _piece(name, first, last):
 @pytest.fixture(scope="module")
 def emulator(tmp_path_factory):
     args = _piece("linear_attention.h", "constexpr int kLaMaxDim", "// Token by token.")
-    body = _piece("linear_recurrent.cu", "constexpr int kLrThreads", "}  // namespace\n\ncudaError_t")
+    body = _piece("linear_recurrent.cu", "constexpr int kLrThreads", "template <bool STEP>\ncudaError_t launch_rows")
     shared = ("    __shared__ float sq[kLaMaxDim], sk[kLaMaxDim];\n"
               "    __shared__ float part[kLrThreads / 32][kLrCols];\n"
               "    __shared__ int next_row;\n")
@@ -107,7 +107,7 @@ def _close(got, want, size, terms, n, out=False):
 
 
 @pytest.mark.parametrize("B,L,G,H,Dk,Dv,per_token", [(1, 1, 1, 1, 8, 8, False), (4, 8, 1, 3, 24, 40, True),
-                                                     (2, 5, 2, 2, 128, 128, False)])
+                                                     (2, 5, 2, 2, 128, 128, False), (1, 3, 1, 2, 56, 8, True)])
 @pytest.mark.parametrize("lengths", [False, True])
 def test_prompts(emulator, tmp_path, B, L, G, H, Dk, Dv, per_token, lengths):
     t = _inputs(B + L, B, L, G, H, Dk, Dv, per_token, B)
