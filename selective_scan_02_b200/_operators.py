@@ -127,12 +127,6 @@ def _on_stream(stream, call, x, *rest):
     return got
 
 
-def _finish(got, what):
-    if got.__class__ is int:
-        _check(got, what)
-    return got
-
-
 def rms_norm(x, weight, residual=None, eps=1e-6, out_dtype=torch.bfloat16, y=None, scales=None, residual_out=None,
              stream=None):
     """Root-mean-square norm with the residual's addition (ss2d_rms_norm).
@@ -144,9 +138,12 @@ def rms_norm(x, weight, residual=None, eps=1e-6, out_dtype=torch.bfloat16, y=Non
     allocated here; a given y keeps its own.  scales (..., ceil(D / 128)) fp32 holds one scale
     for each 128 columns of a row.  residual_out may be `residual` itself.
     """
-    args = (x, weight, residual, eps, out_dtype, y, scales, residual_out)
-    got = _module().rms_norm(*args) if stream is None else _on_stream(stream, _module().rms_norm, *args)
-    return _finish(got, "ss2d_rms_norm")
+    call = (_marshal or _module()).rms_norm
+    if stream is None:
+        got = call(x, weight, residual, eps, out_dtype, y, scales, residual_out)
+    else:
+        got = _on_stream(stream, call, x, weight, residual, eps, out_dtype, y, scales, residual_out)
+    return got if got.__class__ is not int else _check(got, "ss2d_rms_norm")
 
 
 def matmul_fp8(a, a_scales, w, w_scales, bias=None, out_dtype=torch.bfloat16, out=None, workspace=None, stream=None):
@@ -160,9 +157,12 @@ def matmul_fp8(a, a_scales, w, w_scales, bias=None, out_dtype=torch.bfloat16, ou
     matmul_fp8_workspace_size bytes, not shared by calls that overlap on the GPU; allocated here
     when none is given.
     """
-    args = (a, a_scales, w, w_scales, bias, out_dtype, out, workspace)
-    got = _module().matmul_fp8(*args) if stream is None else _on_stream(stream, _module().matmul_fp8, *args)
-    return _finish(got, "ss2d_matmul_fp8")
+    call = (_marshal or _module()).matmul_fp8
+    if stream is None:
+        got = call(a, a_scales, w, w_scales, bias, out_dtype, out, workspace)
+    else:
+        got = _on_stream(stream, call, a, a_scales, w, w_scales, bias, out_dtype, out, workspace)
+    return got if got.__class__ is not int else _check(got, "ss2d_matmul_fp8")
 
 
 def matmul_fp8_workspace_size(M, N, K) -> int:
@@ -185,9 +185,12 @@ def linear_attention(q, k, v, log_decay, scale=1.0, h0=None, lengths=None, retur
     at least linear_attention_workspace_size bytes, not shared by calls that overlap on the GPU;
     allocated here when none is given.
     """
-    args = (q, k, v, log_decay, scale, h0, lengths, return_last_state, out, h_last, workspace)
-    got = _module().linear_attention(*args) if stream is None else _on_stream(stream, _module().linear_attention, *args)
-    return _finish(got, "ss2d_linear_attention")
+    call = (_marshal or _module()).linear_attention
+    if stream is None:
+        got = call(q, k, v, log_decay, scale, h0, lengths, return_last_state, out, h_last, workspace)
+    else:
+        got = _on_stream(stream, call, q, k, v, log_decay, scale, h0, lengths, return_last_state, out, h_last, workspace)
+    return got if got.__class__ is not int else _check(got, "ss2d_linear_attention")
 
 
 def linear_attention_workspace_size(B, L, G, H, Dk, Dv) -> int:
@@ -205,10 +208,12 @@ def linear_attention_step(q, k, v, log_decay, state, slots=None, scale=1.0, out=
     (None: row b has state b); a row whose slot is outside the pool is empty and its row of `out`
     is left as it was, and rows of one slot are consecutive tokens in the order of the rows.
     """
-    args = (q, k, v, log_decay, state, slots, scale, out)
-    got = _module().linear_attention_step(*args) if stream is None else _on_stream(
-        stream, _module().linear_attention_step, *args)
-    return _finish(got, "ss2d_linear_attention_step")
+    call = (_marshal or _module()).linear_attention_step
+    if stream is None:
+        got = call(q, k, v, log_decay, state, slots, scale, out)
+    else:
+        got = _on_stream(stream, call, q, k, v, log_decay, state, slots, scale, out)
+    return got if got.__class__ is not int else _check(got, "ss2d_linear_attention_step")
 
 
 def check_workspace_status(workspace, stream=None):

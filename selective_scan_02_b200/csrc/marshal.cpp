@@ -138,9 +138,9 @@ int fit(int64_t n)
     return (int)n;
 }
 
-std::vector<int64_t> with_last(c10::IntArrayRef shape, int64_t last)
+at::DimVector with_last(c10::IntArrayRef shape, int64_t last)
 {
-    std::vector<int64_t> s(shape.begin(), shape.end());
+    at::DimVector s(shape.begin(), shape.end());
     s.back() = last;
     return s;
 }
@@ -203,7 +203,7 @@ PyObject *rms_norm(PyObject *const *a)
     void *yp = c.dense(y, "y", type, x.sizes());
     float *sp = nullptr;
     if (y_code == SS2D_E4M3) {
-        const std::vector<int64_t> groups = with_last(x.sizes(), (D + kBlock - 1) / kBlock);
+        const at::DimVector groups = with_last(x.sizes(), (D + kBlock - 1) / kBlock);
         if (!scales.defined())
             scales = c.make(groups, at::kFloat);
         sp = c.dense<float>(scales, "scales", at::kFloat, groups);
@@ -238,7 +238,7 @@ PyObject *matmul_fp8(PyObject *const *o)
     args.w = c.dense(w, "w", at::kFloat8_e4m3fn, {N, K});
     args.w_scales = c.dense<float>(w_scales, "w_scales", at::kFloat, {nb, kb});
     args.bias = c.dense<float>(bias, "bias", at::kFloat, {N});
-    const std::vector<int64_t> shape = with_last(a.sizes(), N);
+    const at::DimVector shape = with_last(a.sizes(), N);
     if (!out.defined())
         out = c.make(shape, type);
     args.c = c.dense(out, "out", type, shape);
