@@ -94,7 +94,7 @@ struct Lc {
                               kBarsAt = kDecayAt + kDecays * (uint32_t)sizeof(ChunkDecay);
     // Columns of tensor memory: scores (two buffers; P in place), P V, Q S, and K^T (w V), in as many buffers as
     // there is room for.  Of w V, all three parts in blocks of their own where they fit (one product), else the
-    // first two, and the third is added to the second's (another product).
+    // first two, and the third is added to the second's (a product for each).
     static constexpr uint32_t kScoresAt = 0, kOutAt = 256, kInterAt = kOutAt + DV, kDeltaAt = kInterAt + DV;
     static constexpr int kBlocks = kDeltaAt + kLcParts * DV <= 512 ? kLcParts : kLcParts - 1;
     static constexpr int kDelta = kBlocks * DV, kDeltas = (512 - (int)kDeltaAt) / kDelta;
@@ -396,10 +396,18 @@ __global__ void __launch_bounds__(kLcThreads, 1)
 #pragma unroll
                     for (int x = 0; x < kLcChunk / 32; ++x) {
                         const uint32_t j = half * 4 + x;
-                        tc::mma_bf16(to, kt + j * kStep, w_mn + j * kStep, lc_idesc(C::kDelta, true, true), half > 0 || x > 0);
-                        if (C::kBlocks < kLcParts)
-                            tc::mma_bf16(to + (C::kBlocks - 1) * DV, kt + j * kStep,
-                                         w_mn + C::kBlocks * DV / 64 * (kLcBlock / 16) + j * kStep, lc_idesc(DV, true, true), 1);
+                        if (C::kBlocks == kLcParts) {
+                            tc::mma_bf16(to, kt + j * kStep, w_mn + j * kStep, lc_idesc(C::kDelta, true, true), half > 0 || x > 0);
+                            continue;
+                        }
+                        // A product for each part: MMAs are ordered where their accumulators and shapes are the same, so
+                        // what the third adds to the second's columns has the second's shape.
+#pragma unroll
+                        for (int z = 0; z < kLcParts; ++z) {
+                            const int block = min(z, C::kBlocks - 1);
+                            tc::mma_bf16(to + block * DV, kt + j * kStep, w_mn + z * DV / 64 * (kLcBlock / 16) + j * kStep,
+                                         lc_idesc(DV, true, true), half > 0 || x > 0 || z > block);
+                        }
                     }
                     tc::commit(bar(C::kWeightsFree + half));
                     if (half) {
