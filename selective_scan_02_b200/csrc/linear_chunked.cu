@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         const uint64_t v_mn = tc::swizzled_desc(base + C::kVAt, kLcBlock, 1024);  // MN-major
         LcRing<C::kSlots> tiles, ahead_of;  // of P V, and of the scores
         auto scores = [&](int c) {
-            // the buffer is free: the P V of two chunks before, which reads P in its place, was issued before
+            // (the buffer is free: the P V of two chunks before, which reads P in its place, is done)
             const uint32_t i = ahead_of.slot, round = ahead_of.round, two = c & 1;
             ++ahead_of;
             if (!wait(C::kKFull + i, round) || !wait(C::kQFull + i, round))
@@ -356,8 +356,12 @@ __global__ void __launch_bounds__(kLcThreads, 1)
             const int next = c + 1;
             const bool ahead = next < chunks && ready(C::kKFull + ahead_of.slot, ahead_of.round) &&
                                ready(C::kQFull + ahead_of.slot, ahead_of.round);
-            if (ahead)
+            // their buffer holds the P of the chunk before this one until its P V is done
+            if (ahead) {
+                if (!wait(C::kOutDone, two ^ 1u))
+                    break;
                 scores(next);
+            }
             // P V; P of 16 tokens lies in the first 8 of their 16 columns of the scores
             if (!wait(C::kVFull + i, round) || !wait(C::kVChecked + i, round) || !wait(C::kProbsReady + two, turn) ||
                 !wait(C::kOutFree, two ^ 1u))
@@ -373,7 +377,7 @@ __global__ void __launch_bounds__(kLcThreads, 1)
             }
             __syncwarp();
             if (!ahead && next < chunks)
-                scores(next);
+                scores(next);  // (kOutFree meant that the P V before this one was done)
         }
     } else if (warp == 3) {
         const uint64_t q_k = tc::swizzled_desc(base + C::kQAt, 16, 1024);         // K-major

@@ -109,6 +109,17 @@ def _unordered(trace):
     return bad
 
 
+@pytest.mark.parametrize("ready", [0, 1, 2])
+@pytest.mark.parametrize("dk", [64, 128])
+@pytest.mark.parametrize("dv", [32, 64])
+def test_scores_and_outputs(emulator, dk, dv, ready):
+    """The scores of a chunk replace those that the P V of two chunks before reads its P from."""
+    for chunks in (1, 2, 3, 7):
+        trace = _trace(emulator, dk, dv, False, chunks, ready, 1)
+        assert sum(t[0] == "mma" for t in trace) == chunks * (dk // 16 + 8)
+        assert not _unordered(trace)
+
+
 @pytest.mark.parametrize("states", [False, True])
 @pytest.mark.parametrize("dk", [64, 128])
 @pytest.mark.parametrize("dv", [32, 64])
