@@ -43,10 +43,10 @@ cudaError_t configure_smem(K kernel, int bytes, int *configured)
 
 // Launches a kernel that may be scheduled before the work ahead of it in its stream is done
 // (programmatic dependent launch), in clusters of `cluster` CTAs.  Such a kernel calls
-// grid_wait() in every thread before it reads or writes global memory, and grid_next() when all
-// that it holds of its SM is taken, so that its own successor can be scheduled behind it.  A kernel
-// that needs nothing of the kernel ahead, which itself called grid_wait() before grid_next(), may do
-// without, but for one CTA, which waits before it ends: the end of a kernel means the end of all ahead of it.
+// grid_wait() in every thread before it reads or writes global memory (it waits for the work ahead, and only what stands
+// behind it is promised to see that work's writes), and grid_next() when all that it holds of its SM is taken, so that
+// its own successor can be scheduled behind it.  While it is scheduled early the work ahead still writes, so it
+// reads nothing through the read-only path (__ldg), which may only be given what no one writes during the kernel.
 template <class... P, class... A>
 cudaError_t launch_early(void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t s, int cluster,
                          const A &...args)

@@ -31,7 +31,7 @@
 // Where the heads of all sequences are too few for the GPU, a sequence is cut into segments: a first
 // pass sums each segment's own state (K and V only), a small kernel adds them up along the sequence, each decayed by
 // what lies between, and the pass above starts each segment from the state before it.  The first segment needs no first
-// pass: it goes beside the others' ones.
+// pass: it goes beside the others' ones, in the same launch.
 //
 // What bounds it: a chunk of 128 x 64 columns takes about 3700 cycles.  Shared memory passes 2950 cycles' worth of bytes
 // in them (tiles in, w V out, and the MMAs' operands: 64 columns read all of Q and K), the warps issue 0.6 instructions a
@@ -53,7 +53,8 @@ constexpr int kLcWeight = 4, kLcScore = 12, kLcState = 20, kLcOutput = 28;  // t
 constexpr uint32_t kLcBlock = kLcChunk * 128;  // bytes of 128 tokens by 64 columns of bf16
 constexpr int kLcParts = 3;           // of w V
 constexpr int kLcAhead = 3;           // chunks that a tile is asked for in L2 before its load
-constexpr int kLcIdlePolls = 1 << 24;  // of the copy warp, at 120 ns or more: about 2 s
+constexpr int kLcIdlePolls = 1 << 24;  // of the copy warp and of a second piece, at 120 ns or more: about 2 s
+constexpr int kLcStateWarps = 8;
 constexpr int kLcSms = 148;
 constexpr int kLcMaxSegments = 149;  // one CTA for each SM in either pass
 
@@ -75,11 +76,12 @@ struct ChunkedArgs {
     // (B * H, nseg - 1) its decay
     float *states, *decays;
     int nseg, first_chunks, seg_chunks;  // chunks of the first segment, and of the others
-    int seg_from, segs;                  // the segments of this launch
-    // Cut units (a unit: a CTA's columns of one head of one sequence): the last `cut` ones are in two pieces, the first of
-    // which leaves its state in `states`.  CTAs take the first pieces, the whole units, then the second pieces.
+    int units;                           // of one segment: a CTA's columns of one head of one sequence
+    // Cut units: the last `cut` ones are in two pieces, the first of which leaves its state in `states`.  CTAs take the
+    // first pieces, the whole units, then the second pieces, by tickets: a CTA that has a second piece knows that a CTA
+    // which runs, or has run, has the first.
     int cut, cut_chunks;
-    int launched;        // CTAs of the launch before this one
+    int *tickets;        // those taken; then, of each cut unit, the warps that have stored the first piece's state
 };
 
 template <int DK, int DV>
@@ -154,15 +156,29 @@ __device__ __forceinline__ void lc_store32(void *p, const uint32_t *w)
                  : "memory");
 }
 
-// What a kernel does: all of it; the first pass over segments, which sums their own states alone; all of it with cut
+// What a warp's lanes wrote to global memory before the __syncwarp ahead of the one's lc_release_add is seen by those that
+// read it behind the __syncwarp that follows the other's lc_acquire.
+__device__ __forceinline__ void lc_release_add(int *p)
+{
+    asm volatile("red.release.gpu.global.add.s32 [%0], 1;\n" ::"l"(p) : "memory");
+}
+
+__device__ __forceinline__ int lc_acquire(const int *p)
+{
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];\n" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+// What a CTA does: all of it; the first pass over segments, which sums their own states alone; all of it with cut
 // units; or all of it with the longest sequences first.  The last two are kernels of their own because the few values
 // more that they hold cost the others 3 % of their time (registers).
 enum { kLcAll, kLcStates, kLcCut, kLcSorted };
 
+// `index`: the CTA's place among those of segments seg_from .. seg_from + segs - 1.
 template <int DK, int DV, int PASS>
-__global__ void __launch_bounds__(kLcThreads, 1)
-    linear_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                          const __grid_constant__ CUtensorMap map_v, const ChunkedArgs p)
+__device__ __forceinline__ void linear_chunked(const CUtensorMap &map_q, const CUtensorMap &map_k, const CUtensorMap &map_v,
+                                               const ChunkedArgs &p, int index, int seg_from, int segs)
 {
     using C = Lc<DK, DV>;
     constexpr bool STATES = PASS == kLcStates, CUT = PASS == kLcCut;
@@ -176,23 +192,26 @@ __global__ void __launch_bounds__(kLcThreads, 1)
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
 
     const int slices = (a.Dv + DV - 1) / DV;
-    const int place = (int)blockIdx.x + (CUT ? p.launched : 0), units = a.B * a.H * slices;
+    grid_wait();
+    int place = index;
+    if (CUT) {
+        int *const ticket = reinterpret_cast<int *>(tmem_slot + 1);
+        if (threadIdx.x == 0)
+            *ticket = atomicAdd(p.tickets, 1);
+        __syncthreads();
+        place = *ticket;
+    }
+    const int units = p.units;
     const bool piece0 = CUT && place < p.cut, piece1 = CUT && place >= units;
     const int unit = !CUT ? place : piece0 ? units - p.cut + place : place - p.cut;  // with cut units: one segment
     const int slice = unit % slices;
-    const int seg = p.seg_from + unit / slices % p.segs;
-    long long bh = unit / slices / p.segs;
+    const int seg = seg_from + unit / slices % segs;
+    long long bh = unit / slices / segs;
     const int h = (int)(bh % a.H);
     int b = (int)(bh / a.H);
     const int group = h / (a.H / a.G);
     const int c0 = slice * DV;              // this CTA's columns of v, o and S
     const int cols = min(DV, a.Dv - c0);    // a multiple of 8
-    // What is launched behind the first launch's start needs nothing of it, but for second pieces (and segments), and all
-    // that it reads was there before that began.
-    if (!STATES && (!CUT || p.launched == 0 || piece1))
-        grid_wait();
-    // The launch behind this one waits for this one's end, and means the end of the one before too.
-    const bool holds = STATES && blockIdx.x == gridDim.x - 1;
     if (PASS == kLcSorted) {
         // the sequence that b other ones go before
         const int mine = lane < a.B ? min(max(a.lengths[lane], 0), a.L) : -1;
@@ -207,13 +226,10 @@ __global__ void __launch_bounds__(kLcThreads, 1)
     const int len = a.lengths ? min(max(a.lengths[b], 0), a.L) : a.L;
     const int t_first = (piece1 ? p.cut_chunks : seg == 0 ? 0 : p.first_chunks + (seg - 1) * p.seg_chunks) * kLcChunk;
     const int t_end = min(len, t_first + (piece0 ? p.cut_chunks : seg == 0 ? p.first_chunks : p.seg_chunks) * kLcChunk);
-    if (!STATES && p.seg_from == 0 && place == 0 && threadIdx.x == 0)
+    if (!STATES && seg_from == 0 && place == 0 && threadIdx.x == 0)
         *a.err = 0;  // the call's first kernel, long before any wait of it can run out
-    if (t_first >= len && !(len == 0 && seg == 0 && !piece1)) {
-        if (holds)
-            grid_wait();
+    if (t_first >= len && !(len == 0 && seg == 0 && !piece1))
         return;
-    }
     const int chunks = (t_end - t_first + kLcChunk - 1) / kLcChunk;  // 0 for an empty sequence: its state is kept
 
     if (threadIdx.x == 0) {
@@ -697,6 +713,16 @@ __global__ void __launch_bounds__(kLcThreads, 1)
         const int left = cols - half * kMine;  // columns in this thread, where above 0
         const long long size = (long long)a.Dk * a.Dv, in_head = (long long)row * a.Dv + c0 + half * kMine;
         float *const at_cut = p.states + ((long long)(unit - (units - p.cut)) * a.Dk + row) * DV + half * kMine;
+        int *const stored = p.tickets + 1 + (unit - (units - p.cut));
+        if (piece1) {
+            // the first piece's warps, which run or are done, have all stored their rows
+            int polls = 0;
+            while (lane == 0 && lc_acquire(stored) < kLcStateWarps && polls < kLcIdlePolls) {
+                ++polls;
+                __nanosleep(64);
+            }
+            good = __shfl_sync(0xffffffffu, polls, 0) < kLcIdlePolls;
+        }
         float2 s[kMine / 2];
         auto load = [&](const float *from, float2 (&v)[kMine / 2]) {
 #pragma unroll
@@ -729,7 +755,7 @@ __global__ void __launch_bounds__(kLcThreads, 1)
             publish();
         LcRing<C::kDecays> dec;
         LcRing<C::kDeltas> deltas;
-        for (int c = 0; c < chunks; ++c, ++dec, ++deltas) {
+        for (int c = 0; c < chunks && good; ++c, ++dec, ++deltas) {
             const uint32_t turn = c & 1;
             if (!wait(C::kDecFull + dec.slot, dec.round))
                 break;
@@ -771,10 +797,15 @@ __global__ void __launch_bounds__(kLcThreads, 1)
                 publish();
             }
         }
-        if (good && piece0 && t_end < len && mine)
+        if (good && piece0 && t_end < len) {
+            if (mine)
 #pragma unroll
-            for (int x = 0; x < kMine; x += 4)
-                *reinterpret_cast<float4 *>(at_cut + x) = make_float4(s[x / 2].x, s[x / 2].y, s[x / 2 + 1].x, s[x / 2 + 1].y);
+                for (int x = 0; x < kMine; x += 4)
+                    *reinterpret_cast<float4 *>(at_cut + x) = make_float4(s[x / 2].x, s[x / 2].y, s[x / 2 + 1].x, s[x / 2 + 1].y);
+            __syncwarp();
+            if (lane == 0)
+                lc_release_add(stored);
+        }
         float *const to = !STATES && t_end == len       ? (a.h_last ? a.h_last + bh * size + in_head : nullptr)
                           : STATES || (seg == 0 && p.nseg > 1) ? p.states + (bh * (p.nseg - 1) + seg) * size + in_head
                                                                  : nullptr;
@@ -847,8 +878,37 @@ __global__ void __launch_bounds__(kLcThreads, 1)
     __syncthreads();
     if (warp == 1)
         tc::tmem_free(tmem, 512);
-    if (holds)
-        grid_wait();
+}
+
+template <int DK, int DV, int PASS>
+__global__ void __launch_bounds__(kLcThreads, 1)
+    linear_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                          const __grid_constant__ CUtensorMap map_v, const ChunkedArgs p, int seg_from, int segs)
+{
+    linear_chunked<DK, DV, PASS>(map_q, map_k, map_v, p, (int)blockIdx.x, seg_from, segs);
+}
+
+// All of the first segments, and beside them the first pass over the others but the last ones.
+template <int DK, int DV>
+__global__ void __launch_bounds__(kLcThreads, 1)
+    linear_first_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                        const __grid_constant__ CUtensorMap map_v, const ChunkedArgs p)
+{
+    if ((int)blockIdx.x < p.units)
+        linear_chunked<DK, DV, kLcAll>(map_q, map_k, map_v, p, (int)blockIdx.x, 0, 1);
+    else
+        linear_chunked<DK, DV, kLcStates>(map_q, map_k, map_v, p, (int)blockIdx.x - p.units, 1, p.nseg - 2);
+}
+
+// No ticket taken, nothing stored: ahead of a kernel with cut units.
+constexpr int kLcTicketThreads = 96;
+
+__global__ void __launch_bounds__(kLcTicketThreads) linear_tickets_kernel(int *tickets, int n)
+{
+    grid_next();
+    grid_wait();
+    for (int i = threadIdx.x; i < n; i += kLcTicketThreads)
+        tickets[i] = 0;
 }
 
 // The segments' own states -> the state behind each: one thread for four elements of a head's state, with the
@@ -905,7 +965,9 @@ cudaError_t launch_width(const ChunkedArgs &p, cudaStream_t s)
         e = lc_map(&k, a.k, a.B, a.L, a.G, a.Dk, a.k_batch, a.k_token, a.k_head);
     if (e == cudaSuccess)
         e = lc_map(&v, a.v, a.B, a.L, a.H, a.Dv, a.v_batch, a.v_token, a.v_head);
-    const unsigned units = (unsigned)((long long)a.B * a.H * ((a.Dv + DV - 1) / DV));
+    ChunkedArgs part = p;
+    part.units = (int)((long long)a.B * a.H * ((a.Dv + DV - 1) / DV));
+    const unsigned units = (unsigned)part.units;
     // The longest sequences first, so that the last CTAs to end have little to do, where there is more than one CTA for
     // an SM and a warp can sort them.  (Seven of up to 1531 tokens, 32 heads of 128 x 64: 48.6 us as they come, 46.0 so.)
     const bool sorted = a.lengths && a.B > 1 && a.B <= 32 && p.nseg == 1 && units > (unsigned)kLcSms;
@@ -914,38 +976,27 @@ cudaError_t launch_width(const ChunkedArgs &p, cudaStream_t s)
     if (e == cudaSuccess)
         e = cut ? configure_smem(linear_chunked_kernel<DK, DV, kLcCut>, (int)Lc<DK, DV>::kSmem, configured[2])
                 : configure_smem(whole, (int)Lc<DK, DV>::kSmem, configured[sorted ? 3 : 0]);
+    if (e == cudaSuccess && p.nseg > 1)
+        e = configure_smem(linear_first_kernel<DK, DV>, (int)Lc<DK, DV>::kSmem, configured[1]);
     if (e != cudaSuccess)
         return e;
-    ChunkedArgs part = p;
-    part.segs = 1;
     if (cut) {
-        const unsigned before = units - p.cut;
-        e = launch_early(linear_chunked_kernel<DK, DV, kLcCut>, before, kLcThreads, Lc<DK, DV>::kSmem, s, 1, q, k, v, part);
-        if (e != cudaSuccess)
-            return e;
-        part.launched = (int)before;
-        return launch_early(linear_chunked_kernel<DK, DV, kLcCut>, 2u * p.cut, kLcThreads, Lc<DK, DV>::kSmem, s, 1, q, k, v, part);
+        e = launch_early(linear_tickets_kernel, 1, kLcTicketThreads, 0, s, 1, p.tickets, p.cut + 1);
+        return e != cudaSuccess ? e
+                                : launch_early(linear_chunked_kernel<DK, DV, kLcCut>, units + (unsigned)p.cut, kLcThreads,
+                                               Lc<DK, DV>::kSmem, s, 1, q, k, v, part, 0, 1);
     }
-    e = launch_early(whole, units, kLcThreads, Lc<DK, DV>::kSmem, s, 1, q, k, v, part);
-    if (e != cudaSuccess || p.nseg == 1)
-        return e;
-    part.seg_from = 1;
-    if (p.nseg > 2) {
-        part.segs = p.nseg - 2;
-        e = configure_smem(linear_chunked_kernel<DK, DV, kLcStates>, (int)Lc<DK, DV>::kSmem, configured[1]);
-        if (e == cudaSuccess)
-            e = launch_early(linear_chunked_kernel<DK, DV, kLcStates>, units * part.segs, kLcThreads, Lc<DK, DV>::kSmem, s, 1,
-                             q, k, v, part);
-        const long long elements = (long long)a.B * a.H * a.Dk * a.Dv / 4;
-        if (e == cudaSuccess)
-            e = launch_early(linear_carry_kernel, (unsigned)((elements + kLcCarryThreads - 1) / kLcCarryThreads), kLcCarryThreads,
-                             0, s, 1, p.states, (const float *)p.decays, p.nseg - 1, a.Dk * a.Dv / 4, elements);
-        if (e != cudaSuccess)
-            return e;
-    }
-    part.segs = p.nseg - 1;
-    return launch_early(linear_chunked_kernel<DK, DV, kLcAll>, units * part.segs, kLcThreads, Lc<DK, DV>::kSmem, s, 1, q, k, v,
-                        part);
+    if (p.nseg == 1)
+        return launch_early(whole, units, kLcThreads, Lc<DK, DV>::kSmem, s, 1, q, k, v, part, 0, 1);
+    e = launch_early(linear_first_kernel<DK, DV>, units * (unsigned)(p.nseg - 1), kLcThreads, Lc<DK, DV>::kSmem, s, 1, q, k, v, part);
+    const long long elements = (long long)a.B * a.H * a.Dk * a.Dv / 4;
+    if (e == cudaSuccess)
+        e = launch_early(linear_carry_kernel, (unsigned)((elements + kLcCarryThreads - 1) / kLcCarryThreads), kLcCarryThreads, 0, s,
+                         1, p.states, (const float *)p.decays, p.nseg - 1, a.Dk * a.Dv / 4, elements);
+    if (e == cudaSuccess)
+        e = launch_early(linear_chunked_kernel<DK, DV, kLcAll>, units * (unsigned)(p.nseg - 1), kLcThreads, Lc<DK, DV>::kSmem, s, 1,
+                         q, k, v, part, 1, p.nseg - 1);
+    return e;
 }
 
 // Columns of the state in one CTA.
@@ -958,8 +1009,8 @@ int lc_cols(const LinAttnArgs &a) { return a.Dv <= 32 ? 32 : 64; }
 // 9, 10: 247, 212, 230, 244.  One head of 128 x 64, 65536 tokens, 24, 48, 75, 103: 83, 53, 44, 41.)
 //
 // Where the units fill the last of several waves by half or less, those of that wave are cut in two instead: the first
-// pieces go first, the second ones behind the whole units, when what they start from is long there, and both
-// together fill the SMs.  (Up to 32 sequences with lengths are sorted instead, which evens out more.)
+// pieces go first, the second ones behind the whole units, when what they start from is long there (they wait for it all
+// the same), and both together fill the SMs.  (Up to 32 sequences with lengths are sorted instead, which evens out more.)
 void lc_plan(const LinAttnArgs &a, ChunkedArgs *p)
 {
     const long long units = (long long)a.B * a.H * ((a.Dv + lc_cols(a) - 1) / lc_cols(a));
@@ -998,7 +1049,7 @@ size_t linear_chunked_workspace(const LinAttnArgs &a)
     ChunkedArgs p{};
     lc_plan(a, &p);
     if (p.nseg == 1)
-        return (size_t)p.cut * a.Dk * lc_cols(a) * 4;
+        return p.cut ? round256((size_t)(p.cut + 1) * 4) + (size_t)p.cut * a.Dk * lc_cols(a) * 4 : 0;
     const size_t heads = (size_t)a.B * a.H;
     return round256(heads * (p.nseg - 1) * 4) + heads * (p.nseg - 1) * a.Dk * a.Dv * 4;
 }
@@ -1015,7 +1066,8 @@ cudaError_t launch_linear_chunked(const LinAttnArgs &a, void *workspace, cudaStr
         p.decays = static_cast<float *>(workspace);
         p.states = reinterpret_cast<float *>(static_cast<char *>(workspace) + round256((size_t)heads * (p.nseg - 1) * 4));
     } else if (p.cut) {
-        p.states = static_cast<float *>(workspace);
+        p.tickets = static_cast<int *>(workspace);
+        p.states = reinterpret_cast<float *>(static_cast<char *>(workspace) + round256((size_t)(p.cut + 1) * 4));
     }
     if (lc_cols(a) == 32)
         return a.Dk <= 64 ? launch_width<64, 32>(p, s) : launch_width<128, 32>(p, s);
