@@ -283,13 +283,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
             for (int i = 0; i < W::kCols / 2; ++i)
                 acc[i] = make_float2(0.0f, 0.0f);
-            float s_a = kb0 < kb1 ? __ldg(sa + kb0) : 0.0f, s_w = kb0 < kb1 ? __ldg(sw + kb0) : 0.0f;
+            float s_a = kb0 < kb1 ? sa[kb0] : 0.0f, s_w = kb0 < kb1 ? sw[kb0] : 0.0f;
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const Ring t(it, W::kBuffers);
                 const float s = s_a * s_w;
                 if (kb + 1 < kb1) {  // the next block's scales, on their way meanwhile
-                    s_a = __ldg(sa + kb + 1);
-                    s_w = __ldg(sw + kb + 1);
+                    s_a = sa[kb + 1];
+                    s_w = sw[kb + 1];
                 }
                 good = tc::mbar_wait_warp(done(t.slot), t.round);
                 if (!good)
@@ -333,9 +333,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
                     for (int i = 0; i < W::kCols / 2; ++i) {
                         if (2 * i < cols)
-                            acc[i].x += __ldg(p.bias + n0 + 2 * i);
+                            acc[i].x += p.bias[n0 + 2 * i];
                         if (2 * i + 1 < cols)
-                            acc[i].y += __ldg(p.bias + n0 + 2 * i + 1);
+                            acc[i].y += p.bias[n0 + 2 * i + 1];
                     }
                 fm_store<W::kCols>(p, (size_t)m * p.N + n0, acc, cols);
             }
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     if (p.bias && j < left)
-                        y[j] += __ldg(p.bias + n + j);
+                        y[j] += p.bias[n + j];
                 const size_t to = (size_t)m * p.N + n;
                 if (p.c_bf16) {
                     __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.c) + to;
@@ -510,11 +510,11 @@ __global__ void __launch_bounds__(kNarrowThreads)
         constexpr int kPer = (BT + 31) / 32;
         float next[kPer];
         auto fetch = [&](int kb) {
-            const float w = __ldg(sw + kb);
+            const float w = sw[kb];
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
                 next[i] = lane + 32 * i < BT && t0 + lane + 32 * i < p.M
-                              ? w * __ldg(p.a_scales + (size_t)(t0 + lane + 32 * i) * p.KB + kb)
+                              ? w * p.a_scales[(size_t)(t0 + lane + 32 * i) * p.KB + kb]
                               : 0.0f;
         };
 #pragma unroll
@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(kNarrowThreads)
         __syncthreads();
     if (warp >= 2) {
         const int row = (warp % 4) * 32 + lane, n = n0 + row;
-        const float bias = p.bias && n < p.N ? __ldg(p.bias + n) : 0.0f;
+        const float bias = p.bias && n < p.N ? p.bias[n] : 0.0f;
         const uint32_t from = base + (uint32_t)row * 4;
         for (int t = rank; t < BT && t0 + t < p.M; t += p.split) {
             float y;

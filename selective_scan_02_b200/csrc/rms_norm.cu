@@ -53,7 +53,7 @@ struct Raw8 {
                               : reinterpret_cast<const uint4 *>(static_cast<const float *>(base) + i);
 #pragma unroll
         for (int x = 0; x < kPieces; ++x)
-            v[x] = __ldg(p + x);
+            v[x] = p[x];
     }
     __device__ __forceinline__ void clear()
     {
@@ -134,10 +134,14 @@ __device__ __forceinline__ float rn_scale(float amax)
 // (f32x2) a column takes about eight instructions, which the loads hide.
 enum { kRnNone, kRnF32, kRnBf16 };
 
+// Single columns keep many addresses: 64 registers are the most, or too few rows share an SM (8184 rows of 4100: 128 us
+// with the 89 that the compiler takes by itself, 87 so).
+constexpr int rn_threads(int tpr) { return tpr > kRnThreads ? tpr : kRnThreads; }
+
 template <int TPR, int NV, bool VEC, bool XBF16, int RES>
-__global__ void __launch_bounds__(TPR > kRnThreads ? TPR : kRnThreads) rms_norm_kernel(const RmsArgs a)
+__global__ void __launch_bounds__(rn_threads(TPR), VEC ? 0 : 1024 / rn_threads(TPR)) rms_norm_kernel(const RmsArgs a)
 {
-    constexpr int kThreads = TPR > kRnThreads ? TPR : kRnThreads;
+    constexpr int kThreads = rn_threads(TPR);
     constexpr int kRows = kThreads / TPR;
     constexpr bool kResBf16 = RES == kRnBf16;
     constexpr int kResType = kResBf16 ? SS2D_BF16 : SS2D_F32;
@@ -152,7 +156,26 @@ __global__ void __launch_bounds__(TPR > kRnThreads ? TPR : kRnThreads) rms_norm_
     grid_wait();
     grid_next();
     float2 r[NV][4];
-    Raw8<false> weight[VEC ? NV : 1];
+    // the weights of one of the thread's NV parts: the next one's are loaded as soon as these are used, ahead of the stores
+    // that they would otherwise stand behind
+    float2 w[4];
+    auto weigh = [&](int i) {
+        if (VEC) {
+            Raw8<false> v;
+            v.clear();
+            if ((t + i * TPR) * 8 < a.D)
+                v.load(a.weight, (t + i * TPR) * 8);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[j] = v.pair(j);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = first + (8 * i + 2 * j) * kStep;
+                w[j] = make_float2(c < a.D ? a.weight[c] : 0.0f, c + kStep < a.D ? a.weight[c + kStep] : 0.0f);
+            }
+        }
+    };
     if (VEC) {
         Raw8<XBF16> x[NV];
         Raw8<kResBf16> e[NV];
@@ -166,12 +189,8 @@ __global__ void __launch_bounds__(TPR > kRnThreads ? TPR : kRnThreads) rms_norm_
                     e[i].load(a.residual, at + (t + i * TPR) * 8);
             }
         }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            weight[i].clear();
-            if ((t + i * TPR) * 8 < a.D)
-                weight[i].load(a.weight, (t + i * TPR) * 8);
-        }
+        if (NV <= 2)
+            weigh(0);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
 #pragma unroll
@@ -195,6 +214,7 @@ __global__ void __launch_bounds__(TPR > kRnThreads ? TPR : kRnThreads) rms_norm_
                 if (RES)
                     e[i][j] = in ? rn_load<kResBf16>(a.residual, at + c) : 0.0f;
             }
+        weigh(0);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (RES)
@@ -210,6 +230,8 @@ __global__ void __launch_bounds__(TPR > kRnThreads ? TPR : kRnThreads) rms_norm_
                 r[i][j] = make_float2(f[i][2 * j], f[i][2 * j + 1]);
         }
     }
+    if (VEC && NV > 2)
+        weigh(0);
     float2 squares = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -235,12 +257,14 @@ __global__ void __launch_bounds__(TPR > kRnThreads ? TPR : kRnThreads) rms_norm_
     const float rstd = rsqrtf(sum / (float)a.D + a.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            r[i][j] = __fmul2_rn(r[i][j], w[j]);
+        if (i + 1 < NV)
+            weigh(i + 1);
         if (VEC) {
             const int c = (t + i * TPR) * 8;
             const bool in = live && c < a.D;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                r[i][j] = __fmul2_rn(r[i][j], weight[i].pair(j));
             float k = rstd;
             if (e4m3) {
                 float amax = 0.0f;
@@ -266,7 +290,7 @@ __global__ void __launch_bounds__(TPR > kRnThreads ? TPR : kRnThreads) rms_norm_
 #pragma unroll
                 for (int j = 0; j < kPer; ++j) {
                     const float2 pair = r[i][(h + j) / 2];
-                    f[j] = c + j * kStep < a.D ? (j % 2 ? pair.y : pair.x) * __ldg(a.weight + c + j * kStep) : 0.0f;
+                    f[j] = j % 2 ? pair.y : pair.x;
                     amax = fmaxf(amax, fabsf(f[j]));
                 }
                 float k = rstd;
@@ -288,7 +312,7 @@ __global__ void __launch_bounds__(TPR > kRnThreads ? TPR : kRnThreads) rms_norm_
 template <int TPR, int NV, bool VEC, bool XBF16>
 cudaError_t rms_launch_types(const RmsArgs &a, cudaStream_t s)
 {
-    constexpr int kThreads = TPR > kRnThreads ? TPR : kRnThreads;
+    constexpr int kThreads = rn_threads(TPR);
     const unsigned grid = (unsigned)((a.rows + kThreads / TPR - 1) / (kThreads / TPR));
     if (!a.residual)
         return launch_early(rms_norm_kernel<TPR, NV, VEC, XBF16, kRnNone>, grid, kThreads, 0, s, 1, a);

@@ -60,3 +60,10 @@ def test_kernels_wait_for_the_work_ahead(name):
     assert kernels
     for kernel in kernels:
         assert _waits(src, _body(src, kernel)), kernel
+
+
+@pytest.mark.parametrize("name", FILES)
+def test_nothing_is_read_through_the_read_only_path(name):
+    """ld.global.nc may only read what no one writes while the kernel runs; a kernel that is launched early runs while the
+    work ahead still writes its inputs."""
+    assert not re.search(r"__ldg\b|\.nc\b|__restrict__|__ldlu", _source(name))
