@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kRnGroup = 128;          // columns of one e4m3 scale
 constexpr float kRnE4m3Max = 448.0f;   // largest finite e4m3 value
-constexpr float kRnScaleMin = 7.888609052210118e-31f;  // 2^-100: keeps y / s finite where a group is zero
+constexpr float kRnScaleMin = 7.888609052210118e-31f;  // 2^-100: keeps 1 / s finite where a group is zero
 constexpr int kRnThreads = 256;        // threads of a CTA that holds several rows
 
 struct RmsArgs {
@@ -130,16 +130,16 @@ __device__ __forceinline__ float rn_scale(float amax)
 //   else: single columns, a warp's 256 NV (or the row's) next to one another and 32 of them (or TPR) in the
 //   lanes, so that accesses of rows of any alignment stay together; a group is four of a warp's 32, or eight of 16.
 // The types of x and the residual are the template's, so that all of a thread's loads are issued before
-// the first is used.  y is (r weight) rstd, and q is (r weight) (rstd / s): with the arithmetic in pairs
-// (f32x2) a column takes about eight instructions, which the loads hide.
+// the first is used.  y is (r rstd) weight, and q is y (1 / s): every product stays finite where y and y / s are, s being
+// at least 2^-100.  With the arithmetic in pairs (f32x2) a column takes about eight instructions, which the loads hide.
 enum { kRnNone, kRnF32, kRnBf16 };
 
-// Single columns keep many addresses: 64 registers are the most, or too few rows share an SM (8184 rows of 4100: 128 us
-// with the 89 that the compiler takes by itself, 87 so).
+// Several single columns keep many addresses: 64 registers are the most, or too few rows share an SM (8184 rows of 4100:
+// 128 us with the 89 that the compiler takes by itself, 87 so).
 constexpr int rn_threads(int tpr) { return tpr > kRnThreads ? tpr : kRnThreads; }
 
 template <int TPR, int NV, bool VEC, bool XBF16, int RES>
-__global__ void __launch_bounds__(rn_threads(TPR), VEC ? 0 : 1024 / rn_threads(TPR)) rms_norm_kernel(const RmsArgs a)
+__global__ void __launch_bounds__(rn_threads(TPR), VEC || NV == 1 ? 0 : 1024 / rn_threads(TPR)) rms_norm_kernel(const RmsArgs a)
 {
     constexpr int kThreads = rn_threads(TPR);
     constexpr int kRows = kThreads / TPR;
@@ -259,26 +259,25 @@ __global__ void __launch_bounds__(rn_threads(TPR), VEC ? 0 : 1024 / rn_threads(T
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            r[i][j] = __fmul2_rn(r[i][j], w[j]);
+            r[i][j] = __fmul2_rn(__fmul2_rn(r[i][j], make_float2(rstd, rstd)), w[j]);
         if (i + 1 < NV)
             weigh(i + 1);
         if (VEC) {
             const int c = (t + i * TPR) * 8;
             const bool in = live && c < a.D;
-            float k = rstd;
             if (e4m3) {
                 float amax = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     amax = fmaxf(amax, fmaxf(fabsf(r[i][j].x), fabsf(r[i][j].y)));
-                const float s = rn_scale<TPR < 16 ? TPR : 16>(amax * rstd);
-                k = __fdividef(rstd, s);
+                const float s = rn_scale<TPR < 16 ? TPR : 16>(amax);
+                const float k = __fdividef(1.0f, s);
                 if (in && c % kRnGroup == 0)
                     a.scales[row * a.groups + c / kRnGroup] = s;
-            }
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                r[i][j] = __fmul2_rn(r[i][j], make_float2(k, k));
+                for (int j = 0; j < 4; ++j)
+                    r[i][j] = __fmul2_rn(r[i][j], make_float2(k, k));
+            }
             if (in)
                 rn_store8(a.y, a.y_dtype, at + c, r[i]);
         } else {
@@ -293,10 +292,10 @@ __global__ void __launch_bounds__(rn_threads(TPR), VEC ? 0 : 1024 / rn_threads(T
                     f[j] = j % 2 ? pair.y : pair.x;
                     amax = fmaxf(amax, fabsf(f[j]));
                 }
-                float k = rstd;
+                float k = 1.0f;
                 if (e4m3) {
-                    const float s = rn_scale<kStep>(amax * rstd);
-                    k = __fdividef(rstd, s);
+                    const float s = rn_scale<kStep>(amax);
+                    k = __fdividef(1.0f, s);
                     if (live && t % kStep == 0 && c < a.D)
                         a.scales[row * a.groups + c / kRnGroup] = s;
                 }
