@@ -114,14 +114,18 @@ __device__ __forceinline__ void rn_store(void *base, int dtype, long long at, fl
         static_cast<uint8_t *>(base)[at] = __nv_cvt_float_to_fp8(f, __NV_SATFINITE, __NV_E4M3);
 }
 
-// The scale of a group, from the maximum over LANES neighbouring lanes.
+// The scale of a group, from the maximum over LANES neighbouring lanes: max / 448, rounded once.  (The product with the
+// rounded reciprocal, corrected by what it leaves, which is exact in an fma: Markstein's division.  An ordinary
+// one takes 2^25 elements in rows of 4100 columns from 90 to 103 us.)
 template <int LANES>
 __device__ __forceinline__ float rn_scale(float amax)
 {
 #pragma unroll
     for (int d = LANES / 2; d > 0; d /= 2)
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-    return fmaxf(amax * (1.0f / kRnE4m3Max), kRnScaleMin);
+    const float inverse = 1.0f / kRnE4m3Max, near = amax * inverse;
+    const float left = fmaf(-kRnE4m3Max, near, amax);
+    return fmaxf(amax < INFINITY ? fmaf(left, inverse, near) : amax, kRnScaleMin);
 }
 
 // TPR threads hold a row, each 8 NV of its columns.
@@ -271,7 +275,7 @@ __global__ void __launch_bounds__(rn_threads(TPR), VEC || NV == 1 ? 0 : 1024 / r
                 for (int j = 0; j < 4; ++j)
                     amax = fmaxf(amax, fmaxf(fabsf(r[i][j].x), fabsf(r[i][j].y)));
                 const float s = rn_scale<TPR < 16 ? TPR : 16>(amax);
-                const float k = __fdividef(1.0f, s);
+                const float k = 1.0f / s;
                 if (in && c % kRnGroup == 0)
                     a.scales[row * a.groups + c / kRnGroup] = s;
 #pragma unroll
@@ -295,7 +299,7 @@ __global__ void __launch_bounds__(rn_threads(TPR), VEC || NV == 1 ? 0 : 1024 / r
                 float k = 1.0f;
                 if (e4m3) {
                     const float s = rn_scale<kStep>(amax);
-                    k = __fdividef(1.0f, s);
+                    k = 1.0f / s;
                     if (live && t % kStep == 0 && c < a.D)
                         a.scales[row * a.groups + c / kRnGroup] = s;
                 }

@@ -181,3 +181,20 @@ def test_small_rows_with_a_small_eps(emulator, tmp_path, D):
             got = _run(emulator, tmp_path, x, w, res, F32, rt, yt, eps, True)
             assert np.isfinite(got[0]).all(), eps
             _check(got, x, w, res, rt, yt, eps)
+
+
+def test_scales_are_rounded_once(emulator, tmp_path):
+    """Rows of plus and minus one have a norm of one, so that y is the weight itself: the scale is the quotient of its group's
+    maximum and 448, rounded once, and no column is further from its value than the rounding to e4m3 of a quotient that is
+    itself within a step of fp32."""
+    rng = np.random.default_rng(3)
+    for D, many in ((512, True), (1301, True)):
+        x = rng.choice(np.array([-1, 1], np.float32), (4, D))
+        w = rng.standard_normal(D).astype(np.float32)
+        q, s, _ = _run(emulator, tmp_path, x, w, None, BF, None, F8, 0.0, many)
+        amax = np.pad(np.abs(w), (0, -D % 128)).reshape(-1, 128).max(-1)
+        want = (amax.astype(np.float64) / 448).astype(np.float32)
+        assert (s == want).all()
+        t = np.abs(x * w / np.repeat(want, 128)[:D].astype(np.float64))
+        unit = 2.0 ** (np.floor(np.log2(np.maximum(t, 2.0 ** -6))) - 3)
+        assert (np.abs(np.abs(q) - t) <= unit / 2 + 3 * U * t).all()
