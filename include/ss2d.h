@@ -489,8 +489,8 @@ size_t ss2d_linear_attention_workspace(const ss2d_linear_attention_args *args);
 
 /* The attention above.  workspace: as for ss2d_matmul_fp8.
  * Log decays below -128 count as -128 (a decay of zero in fp32), so -infinity resets the state.
- * An infinity or a NaN in q, k or v makes what its token enters not finite (a NaN, or an infinity), and
- * reaches no earlier token and, of v, no other column.
+ * An infinity or a NaN in q, k or v, or a NaN in log_decay, makes what its token enters not finite (a NaN, or an
+ * infinity), and reaches no earlier token and, of v, no other column.
  * The state and the sums are fp32; q, k, v and out are bf16.  Deterministic. */
 int ss2d_linear_attention(const ss2d_linear_attention_args *args, void *workspace, size_t workspace_bytes,
                           void *stream);

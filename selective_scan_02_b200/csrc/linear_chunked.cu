@@ -472,14 +472,24 @@ __device__ __forceinline__ void linear_chunked(const CUtensorMap &map_q, const C
             fetch(0);
         LcRing<C::kDecays> dec;
         for (int c = 0; c < chunks; ++c, ++dec) {
+            // A NaN enters no sum, or it would reach the tokens before it: cb is one from its token on, and the weights and
+            // rows that follow from cb carry it to the outputs and the state.
+            int nan_at = 4;
+#pragma unroll
+            for (int j = 3; j >= 0; --j) {
+                if (g[j] != g[j])
+                    nan_at = j;
+                g[j] = fmaxf(g[j], kLaMinLogDecay);
+            }
+            const unsigned bad = __ballot_sync(0xffffffffu, nan_at < 4);
             // cb_j, the sum from a block's end back to j, added from the end: where a weight exp(-cb) counts, cb is
             // small, and so is its rounding.  The same for the blocks within the chunk.
             float after[4];  // of the lane's tokens: the lane's later ones
             after[3] = 0.0f;
 #pragma unroll
             for (int j = 2; j >= 0; --j)
-                after[j] = after[j + 1] + la_clamp(g[j + 1]) * kLcLog2e;
-            const float own = after[0] + la_clamp(g[0]) * kLcLog2e;
+                after[j] = after[j + 1] + g[j + 1] * kLcLog2e;
+            const float own = after[0] + g[0] * kLcLog2e;
             if (c + 1 < chunks)
                 fetch(c + 1);
             float sum = own;  // of this lane and the block's later ones
@@ -503,6 +513,13 @@ __device__ __forceinline__ void linear_chunked(const CUtensorMap &map_q, const C
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 cb[j] = -(later + after[j]);
+            if (bad) {
+                const int first = __ffs(bad) - 1;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (lane > first || (lane == first && j >= nan_at))
+                        cb[j] = __int_as_float(0x7fffffff);
+            }
             *reinterpret_cast<float4 *>(&out.cb[lane * 4]) = make_float4(cb[0], cb[1], cb[2], cb[3]);
             *reinterpret_cast<float4 *>(&out.f[lane * 4]) =
                 make_float4(exp2f(-cb[0]), exp2f(-cb[1]), exp2f(-cb[2]), exp2f(-cb[3]));
