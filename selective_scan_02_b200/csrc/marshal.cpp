@@ -145,6 +145,17 @@ at::DimVector with_last(c10::IntArrayRef shape, int64_t last)
     return s;
 }
 
+// A call of the C ABI without the interpreter's lock, as ctypes makes the library's other calls: a launch waits where the
+// queue of launches is full, and the status for its stream, while other threads (and the stream's host callbacks) go on.
+template <class F>
+int unlocked(const F &call)
+{
+    PyThreadState *const state = PyEval_SaveThread();
+    const int status = call();
+    PyEval_RestoreThread(state);
+    return status;
+}
+
 // Python values of a call: the status where it is not SS2D_OK, else the tensors.
 PyObject *result(int status, std::initializer_list<at::Tensor> tensors)
 {
@@ -210,8 +221,10 @@ PyObject *rms_norm(PyObject *const *a)
     } else if (scales.defined()) {
         refuse("scales is given without a float8_e4m3fn y");
     }
-    return result(ss2d_rms_norm(xp, x_code, rp, r_code, wp, (float)eps, yp, y_code, sp, rop, rows, fit(D), c.stream),
-                  {y, scales, residual_out});
+    const int columns = fit(D);
+    const int status = unlocked(
+        [&] { return ss2d_rms_norm(xp, x_code, rp, r_code, wp, (float)eps, yp, y_code, sp, rop, rows, columns, c.stream); });
+    return result(status, {y, scales, residual_out});
 }
 
 // matmul_fp8(a, a_scales, w, w_scales, bias, out_dtype, out, workspace)
@@ -246,7 +259,7 @@ PyObject *matmul_fp8(PyObject *const *o)
     if (need == (size_t)-1)  // the call says what is wrong with its arguments
         return result(ss2d_matmul_fp8(&args, nullptr, 0, c.stream), {});
     const at::Tensor ws = c.workspace(given, need);
-    return result(ss2d_matmul_fp8(&args, ws.data_ptr(), ws.nbytes(), c.stream), {out});
+    return result(unlocked([&] { return ss2d_matmul_fp8(&args, ws.data_ptr(), ws.nbytes(), c.stream); }), {out});
 }
 
 void heads(const at::Tensor &q, const at::Tensor &v, int64_t dims, const char *shapes)
@@ -291,7 +304,7 @@ PyObject *linear_attention(PyObject *const *o)
     if (need == (size_t)-1)
         return result(ss2d_linear_attention(&args, nullptr, 0, c.stream), {});
     const at::Tensor ws = c.workspace(given, need);
-    return result(ss2d_linear_attention(&args, ws.data_ptr(), ws.nbytes(), c.stream), {out, h_last});
+    return result(unlocked([&] { return ss2d_linear_attention(&args, ws.data_ptr(), ws.nbytes(), c.stream); }), {out, h_last});
 }
 
 // linear_attention_step(q, k, v, log_decay, state, slots, scale, out)
@@ -324,7 +337,7 @@ PyObject *linear_attention_step(PyObject *const *o)
     if (!out.defined())
         out = c.make({B, H, Dv}, at::kBFloat16);
     args.out = c.dense(out, "out", at::kBFloat16, {B, H, Dv});
-    return result(ss2d_linear_attention_step(&args, c.stream), {out});
+    return result(unlocked([&] { return ss2d_linear_attention_step(&args, c.stream); }), {out});
 }
 
 // workspace_status(workspace)
@@ -332,7 +345,7 @@ PyObject *workspace_status(PyObject *const *o)
 {
     const at::Tensor ws = tensor(o[0], "workspace");
     const Call c(ws);
-    return PyLong_FromLong(ss2d_workspace_status(ws.data_ptr(), c.stream));
+    return PyLong_FromLong(unlocked([&] { return ss2d_workspace_status(ws.data_ptr(), c.stream); }));
 }
 
 template <PyObject *(*F)(PyObject *const *), Py_ssize_t N>
