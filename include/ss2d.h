@@ -24,8 +24,8 @@
  *   - All tensors are dense, row-major, in device memory owned by the caller.
  *     The library never allocates device memory and never synchronises the
  *     device (the exceptions are the diagnostics ss2d_device_status,
- *     ss2d_block_device_status and ss2d_workspace_status, which wait for their
- *     stream); work is enqueued on `stream` (a cudaStream_t; NULL is
+ *     ss2d_block_device_status, ss2d_workspace_status and ss2d_wait_status,
+ *     which wait for their stream); work is enqueued on `stream` (a cudaStream_t; NULL is
  *     the legacy default stream) and runs asynchronously.
  *   - Every tensor pointer must be 16-byte aligned; otherwise the call returns
  *     SS2D_ERR_MISALIGNED and enqueues nothing.
@@ -526,6 +526,17 @@ int ss2d_linear_attention_step(const ss2d_linear_attention_step_args *args, void
  * SS2D_OK, or SS2D_ERR_DEVICE if a bounded wait of a tensor-core kernel ran out, in which case
  * that call's outputs are not valid.  Synchronises `stream`. */
 int ss2d_workspace_status(const void *workspace, void *stream);
+
+/* The same of the current device, whatever the workspaces were: SS2D_ERR_DEVICE if a bounded wait of any
+ * ss2d_matmul_fp8 or ss2d_linear_attention on it ran out, up to the work ahead in `stream`, since the last
+ * ss2d_wait_status that said so.  Synchronises `stream`. */
+int ss2d_wait_status(void *stream);
+
+/* Diagnostic, as ss2d_diag_bounded_wait: runs the error path of these operators' bounded waits on purpose.  One CTA
+ * waits on an mbarrier that nothing arrives at for spin_limit polls (1 .. 2^19), in both forms that their kernels wait
+ * in, then does what they do: sets the error word of `workspace` (any of at least 4 bytes, 16-byte aligned) and
+ * the device's, frees its tensor memory and returns.  ss2d_workspace_status and ss2d_wait_status then report it. */
+int ss2d_diag_operator_wait(void *workspace, long long spin_limit, void *stream);
 
 #ifdef __cplusplus
 }

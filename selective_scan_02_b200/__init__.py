@@ -38,6 +38,7 @@ from ._operators import (  # noqa: F401
     LinearAttentionStepArgs,
     MatmulFp8Args,
     check_workspace_status,
+    diag_operator_wait,
     linear_attention,
     linear_attention_step,
     linear_attention_workspace_size,
@@ -52,6 +53,6 @@ __all__ = [
     "forward_core_backward", "forward_core_backward_workspace_size", "forward_core_static",
     "forward_core_workspace_size", "load_library", "selective_scan",
     "SS2D_E4M3", "LinearAttentionArgs", "LinearAttentionStepArgs", "MatmulFp8Args", "check_workspace_status",
-    "linear_attention", "linear_attention_step", "linear_attention_workspace_size", "matmul_fp8",
+    "diag_operator_wait", "linear_attention", "linear_attention_step", "linear_attention_workspace_size", "matmul_fp8",
     "matmul_fp8_workspace_size", "rms_norm",
 ]

@@ -86,6 +86,10 @@ def _library():
         lib.ss2d_linear_attention_step.restype = I
         lib.ss2d_workspace_status.argtypes = [P, P]
         lib.ss2d_workspace_status.restype = I
+        lib.ss2d_wait_status.argtypes = [P]
+        lib.ss2d_wait_status.restype = I
+        lib.ss2d_diag_operator_wait.argtypes = [P, ctypes.c_longlong, P]
+        lib.ss2d_diag_operator_wait.restype = I
         _lib = lib
     return _lib
 
@@ -216,9 +220,27 @@ def linear_attention_step(q, k, v, log_decay, state, slots=None, scale=1.0, out=
     return got if got.__class__ is not int else _check(got, "ss2d_linear_attention_step")
 
 
-def check_workspace_status(workspace, stream=None):
-    """Raises Ss2dError (SS2D_ERR_DEVICE) if a tensor-core kernel's bounded wait ran out in the last
-    matmul_fp8 or linear_attention on `workspace` (ss2d_workspace_status).  Synchronises the stream."""
+def check_workspace_status(workspace=None, stream=None):
+    """Raises Ss2dError (SS2D_ERR_DEVICE) if a tensor-core kernel's bounded wait ran out: in the last
+    matmul_fp8 or linear_attention on `workspace` (ss2d_workspace_status), or, with none, in any such call on the
+    stream's device (the current one), with workspaces of whatever origin, since this was last reported
+    (ss2d_wait_status).  Synchronises the stream."""
+    if workspace is None:
+        stream = torch.cuda.current_stream() if stream is None else stream
+        with torch.cuda.device(stream.device):
+            _check(_library().ss2d_wait_status(ctypes.c_void_p(stream.cuda_stream)), "ss2d_wait_status")
+        return
     got = _module().workspace_status(workspace) if stream is None else _on_stream(
         stream, _module().workspace_status, workspace)
     _check(got, "ss2d_workspace_status")
+
+
+def diag_operator_wait(workspace, spin_limit, stream=None):
+    """ss2d_diag_operator_wait: the operators' tensor-core waits run out on purpose after spin_limit polls, which is
+    noted in the workspace's error word and the device's (for testing failure reporting)."""
+    if not workspace.is_cuda or not workspace.is_contiguous() or workspace.nbytes < 4:
+        raise ValueError("workspace must be a contiguous device tensor of at least 4 bytes")
+    with torch.cuda.device(workspace.device):
+        stream = torch.cuda.current_stream() if stream is None else stream
+        _check(_library().ss2d_diag_operator_wait(workspace.data_ptr(), int(spin_limit), ctypes.c_void_p(stream.cuda_stream)),
+               "ss2d_diag_operator_wait")

@@ -8,8 +8,11 @@
 // error word exactly as the GEMM kernels do, frees the tensor memory and returns.
 #include <stdint.h>
 
+#include "op_check.h"
 #include "ss2d.h"
 #include "tcgen05.cuh"
+#include "tma.cuh"
+#include "wait_status.cuh"
 
 namespace ss2d {
 namespace {
@@ -44,8 +47,60 @@ __global__ void bounded_wait_probe_kernel(int *err, long long limit)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(32));
 }
 
+// The same for the operators' kernels, whose warps wait one lane alone (copies) or together (all else).
+__global__ void operator_wait_probe_kernel(int *err, uint32_t limit)
+{
+    __shared__ __align__(8) uint64_t mbar;
+    __shared__ uint32_t tmem_slot;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        tc::mbar_init(tc::smem_u32(&mbar), 1);
+        tc::mbar_init_fence();
+        *err = 0;
+    }
+    if (warp == 1)
+        tc::tmem_alloc(&tmem_slot, 32);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = tmem_slot;
+    bool good = true;
+    if (warp == 0) {
+        if (lane == 0)
+            good = tc::mbar_wait(tc::smem_u32(&mbar), 0u, limit);
+    } else {
+        good = tc::mbar_wait_warp(tc::smem_u32(&mbar), 0u, limit);
+    }
+    if (!good && lane == 0)
+        wait_ran_out(err);
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 1)
+        tc::tmem_free(tmem, 32);
+}
+
 }  // namespace
+
+cudaError_t diag_wait_ran_out(bool *out, cudaStream_t s) { return take_wait_ran_out(out, s); }
+
 }  // namespace ss2d
+
+extern "C" int ss2d_diag_operator_wait(void *workspace, long long spin_limit, void *stream)
+{
+    using namespace ss2d;
+    static const char *call = "ss2d_diag_operator_wait";
+    set_last_error(SS2D_OK, "");
+    if (!workspace)
+        return op_fail(SS2D_ERR_WORKSPACE, "%s: a workspace is required", call);
+    if (reinterpret_cast<uintptr_t>(workspace) & 15u)
+        return op_fail(SS2D_ERR_MISALIGNED, "%s: workspace must be 16-byte aligned", call);
+    if (spin_limit < 1 || spin_limit > (1LL << 19))  // at most about 4 s of polling, one warp's behind the other's
+        return op_fail(SS2D_ERR_INVALID_ARG, "%s: spin_limit=%lld is not within 1 and 2^19", call, spin_limit);
+    operator_wait_probe_kernel<<<1, 64, 0, static_cast<cudaStream_t>(stream)>>>(static_cast<int *>(workspace), (uint32_t)spin_limit);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? SS2D_OK : op_cuda_fail(e, "ss2d_diag_operator_wait launch");
+}
 
 extern "C" int ss2d_diag_bounded_wait(int *error_word, long long spin_limit, void *stream)
 {

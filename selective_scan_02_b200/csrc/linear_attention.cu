@@ -4,6 +4,7 @@
 
 #include "op_check.h"
 #include "ss2d.h"
+#include "wait_words.h"
 
 namespace ss2d {
 namespace {
@@ -210,5 +211,25 @@ extern "C" int ss2d_workspace_status(const void *workspace, void *stream)
     if (flag != 0)
         return op_fail(SS2D_ERR_DEVICE, "%s: a tensor-core kernel's bounded wait ran out; that call's outputs are not valid",
                        call);
+    return SS2D_OK;
+}
+
+extern "C" int ss2d_wait_status(void *stream)
+{
+    using namespace ss2d;
+    static const char *call = "ss2d_wait_status";
+    set_last_error(SS2D_OK, "");
+    bool out = false;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = matmul_fp8_wait_ran_out(&out, s);
+    if (e == cudaSuccess)
+        e = linear_chunked_wait_ran_out(&out, s);
+    if (e == cudaSuccess)
+        e = diag_wait_ran_out(&out, s);
+    if (e != cudaSuccess)
+        return op_cuda_fail(e, "ss2d_wait_status read");
+    if (out)
+        return op_fail(SS2D_ERR_DEVICE, "%s: a tensor-core kernel's bounded wait ran out on this device; the outputs of some call "
+                                        "since the last ss2d_wait_status are not valid", call);
     return SS2D_OK;
 }

@@ -43,6 +43,7 @@
 #include "launch_util.h"
 #include "linear_attention.h"
 #include "tma.cuh"
+#include "wait_status.cuh"
 
 namespace ss2d {
 namespace {
@@ -889,7 +890,7 @@ __device__ __forceinline__ void linear_chunked(const CUtensorMap &map_q, const C
         }
     }
     if (!good && lane == 0)
-        atomicExch(a.err, 1);
+        wait_ran_out(a.err);
     __syncwarp();
     tc::fence_before();
     __syncthreads();
@@ -1060,6 +1061,8 @@ void lc_plan(const LinAttnArgs &a, ChunkedArgs *p)
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
+
+cudaError_t linear_chunked_wait_ran_out(bool *out, cudaStream_t s) { return take_wait_ran_out(out, s); }
 
 size_t linear_chunked_workspace(const LinAttnArgs &a)
 {

@@ -345,6 +345,8 @@ PyObject *workspace_status(PyObject *const *o)
 {
     const at::Tensor ws = tensor(o[0], "workspace");
     const Call c(ws);
+    if (!ws.is_contiguous() || ws.nbytes() < sizeof(int))
+        refuse("workspace must be a contiguous tensor that holds the error word (4 bytes)");
     return PyLong_FromLong(unlocked([&] { return ss2d_workspace_status(ws.data_ptr(), c.stream); }));
 }
 

@@ -33,6 +33,7 @@
 #include "op_check.h"
 #include "ss2d.h"
 #include "tma.cuh"
+#include "wait_status.cuh"
 
 namespace ss2d {
 namespace {
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
     }
     if (!good && lane == 0)
-        atomicExch(p.err, 1);
+        wait_ran_out(p.err);
     __syncwarp();
     tc::fence_before();
     __syncthreads();
@@ -561,7 +562,7 @@ __global__ void __launch_bounds__(kNarrowThreads)
         }
     }
     if (!good && lane == 0)
-        atomicExch(p.err, 1);
+        wait_ran_out(p.err);
     __syncwarp();
     tc::fence_before();
     __syncthreads();  // every MMA and copy of this CTA is done: its stages are free
@@ -716,6 +717,9 @@ int fm_check(const char *call, const ss2d_matmul_fp8_args *a)
 }
 
 }  // namespace
+
+cudaError_t matmul_fp8_wait_ran_out(bool *out, cudaStream_t s) { return take_wait_ran_out(out, s); }
+
 }  // namespace ss2d
 
 extern "C" size_t ss2d_matmul_fp8_workspace(const ss2d_matmul_fp8_args *args)

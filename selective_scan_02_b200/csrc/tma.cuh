@@ -47,7 +47,7 @@ __device__ __forceinline__ bool elect_one()
 
 // mbar_wait for a warp that waits together (all lanes poll, all lanes agree on the result), with the bound
 // of tcgen05.cuh.
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t mbar, uint32_t phase)
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t mbar, uint32_t phase, uint32_t limit = (uint32_t)kSpinLimit)
 {
     uint32_t done;
     asm volatile(
@@ -62,7 +62,7 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t mbar, uint32_t phase)
         "DONE:\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}\n"
         : "=r"(done)
-        : "r"(mbar), "r"(phase), "n"((uint32_t)kSpinLimit)
+        : "r"(mbar), "r"(phase), "r"(limit)
         : "memory");
     return __all_sync(0xffffffffu, done);
 }

@@ -187,3 +187,12 @@ def test_workspace_sizes_refuse_bad_sizes():
         ss.matmul_fp8_workspace_size(4, 4, 8)
     with pytest.raises(ss.Ss2dError):
         ss.linear_attention_workspace_size(1, 0, 1, 1, 8, 8)
+
+
+def test_diag_operator_wait_refusals(lib):
+    assert lib.ss2d_diag_operator_wait(None, 1, None) == WORKSPACE
+    assert lib.ss2d_diag_operator_wait(FAKE + 4, 1, None) == MISALIGNED
+    assert lib.ss2d_diag_operator_wait(FAKE, 0, None) == INVALID
+    assert lib.ss2d_diag_operator_wait(FAKE, (1 << 19) + 1, None) == INVALID
+    with pytest.raises(ValueError):
+        ss.diag_operator_wait(torch.zeros(16, dtype=torch.uint8), 1)
