@@ -28,7 +28,9 @@
  *     which wait for their stream); work is enqueued on `stream` (a cudaStream_t; NULL is
  *     the legacy default stream) and runs asynchronously.
  *   - Every tensor pointer must be 16-byte aligned; otherwise the call returns
- *     SS2D_ERR_MISALIGNED and enqueues nothing.
+ *     SS2D_ERR_MISALIGNED and enqueues nothing.  (Of the linear-attention
+ *     layer's operators the scales, bias, lengths and slots may lie on any
+ *     4 bytes: slices of longer arrays.)
  *   - Arguments are checked on the host before anything is enqueued.  A
  *     failed check returns its status and leaves all buffers untouched.
  *     A failed launch returns SS2D_ERR_CUDA.  The text of the last failure

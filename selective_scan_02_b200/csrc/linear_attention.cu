@@ -109,7 +109,7 @@ extern "C" int ss2d_linear_attention(const ss2d_linear_attention_args *args, voi
         {"k", a.k, la_span(a.B, a.k_stride[0], a.L, a.k_stride[1], a.G, a.k_stride[2], a.Dk)},
         {"v", a.v, la_span(a.B, a.v_stride[0], a.L, a.v_stride[1], a.H, a.v_stride[2], a.Dv)},
         {"log_decay", a.log_decay, (a.decay_per_token ? BH * a.L : (size_t)a.H) * 4},
-        {"lengths", a.lengths, (size_t)a.B * 4},
+        {"lengths", a.lengths, (size_t)a.B * 4, 4},
         // a state may be replaced in place: each element is read and then written by the same thread
         {"h0", a.h0, a.h0 == a.h_last ? 0 : state}};
     const OpSpan out[] = {{"out", a.out, BH * a.L * a.Dv * 2}, {"h_last", a.h_last, state}, {"workspace", workspace, need}};
@@ -168,7 +168,7 @@ extern "C" int ss2d_linear_attention_step(const ss2d_linear_attention_step_args 
                          {"k", a.k, la_span(a.B, a.k_stride[0], 1, 0, a.G, a.k_stride[1], a.Dk)},
                          {"v", a.v, la_span(a.B, a.v_stride[0], 1, 0, a.H, a.v_stride[1], a.Dv)},
                          {"log_decay", a.log_decay, (a.decay_per_token ? BH : (size_t)a.H) * 4},
-                         {"slots", a.slots, (size_t)a.B * 4}};
+                         {"slots", a.slots, (size_t)a.B * 4, 4}};
     const OpSpan out[] = {{"out", a.out, BH * a.Dv * 2}, {"state", a.state, (size_t)a.pool * a.H * a.Dk * a.Dv * 4}};
     st = op_check_tensors(call, in, 5, out, 2);
     if (st != SS2D_OK)

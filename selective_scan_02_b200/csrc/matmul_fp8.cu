@@ -744,10 +744,10 @@ extern "C" int ss2d_matmul_fp8(const ss2d_matmul_fp8_args *args, void *workspace
         return op_fail(SS2D_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", call, kFmWorkspace,
                        workspace_bytes);
     const OpSpan in[] = {{"a", args->a, M * K},
-                         {"a_scales", args->a_scales, M * KB * 4},
+                         {"a_scales", args->a_scales, M * KB * 4, 4},
                          {"w", args->w, N * K},
-                         {"w_scales", args->w_scales, (N + kFmBlock - 1) / kFmBlock * KB * 4},
-                         {"bias", args->bias, N * 4}};
+                         {"w_scales", args->w_scales, (N + kFmBlock - 1) / kFmBlock * KB * 4, 4},
+                         {"bias", args->bias, N * 4, 4}};
     const size_t esize = args->c_dtype == SS2D_BF16 ? 2 : 4;
     const OpSpan out[] = {{"c", args->c, M * N * esize}, {"workspace", workspace, kFmWorkspace}};
     st = op_check_tensors(call, in, 5, out, 2);

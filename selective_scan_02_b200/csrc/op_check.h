@@ -31,6 +31,7 @@ struct OpSpan {
     const char *name;
     const void *p;  // nullptr: an optional tensor that is not given
     size_t bytes;
+    unsigned align = 16;  // 4 for what is accessed one number at a time
 };
 
 inline bool op_overlaps(const OpSpan &a, const OpSpan &b)
@@ -41,14 +42,14 @@ inline bool op_overlaps(const OpSpan &a, const OpSpan &b)
     return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
 }
 
-// Checks of one call's tensors: 16-byte alignment of every one, then no output overlapping an
+// Checks of one call's tensors: the alignment of every one, then no output overlapping an
 // input or another output.  Returns SS2D_OK or the status, with the error text set.
 inline int op_check_tensors(const char *call, const OpSpan *in, int n_in, const OpSpan *out, int n_out)
 {
     for (int i = 0; i < n_in + n_out; ++i) {
         const OpSpan &t = i < n_in ? in[i] : out[i - n_in];
-        if (reinterpret_cast<uintptr_t>(t.p) & 15u)
-            return op_fail(SS2D_ERR_MISALIGNED, "%s: %s must be 16-byte aligned", call, t.name);
+        if (reinterpret_cast<uintptr_t>(t.p) & (t.align - 1))
+            return op_fail(SS2D_ERR_MISALIGNED, "%s: %s must be %u-byte aligned", call, t.name, t.align);
     }
     for (int o = 0; o < n_out; ++o) {
         for (int i = 0; i < n_in; ++i)

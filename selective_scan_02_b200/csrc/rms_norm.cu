@@ -371,7 +371,7 @@ extern "C" int ss2d_rms_norm(const void *x, int x_dtype, const void *residual, i
                          // the residual may be updated in place: it is read and written by the same thread
                          {"residual", residual, residual == residual_out ? 0 : n * rms_esize(residual_dtype)}};
     const OpSpan out[] = {{"y", y, n * rms_esize(y_dtype)},
-                          {"scales", scales, (size_t)rows * groups * 4},
+                          {"scales", scales, (size_t)rows * groups * 4, 4},
                           {"residual_out", residual_out, n * rms_esize(residual_dtype)}};
     const int st = op_check_tensors(call, in, 3, out, 3);
     if (st != SS2D_OK)

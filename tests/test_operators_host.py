@@ -196,3 +196,22 @@ def test_diag_operator_wait_refusals(lib):
     assert lib.ss2d_diag_operator_wait(FAKE, (1 << 19) + 1, None) == INVALID
     with pytest.raises(ValueError):
         ss.diag_operator_wait(torch.zeros(16, dtype=torch.uint8), 1)
+
+
+def test_what_is_read_number_by_number_may_lie_on_four_bytes(lib):
+    """A refusal that comes behind the alignment's (an overlap of the outputs) shows that the alignment was accepted."""
+    ws = FAKE + 40 * GB
+
+    def accepted(status):
+        return status == INVALID and b"overlaps" in lib.ss2d_last_error()
+
+    for name in ("a_scales", "w_scales", "bias"):
+        at = getattr(_matmul(), name)
+        assert accepted(lib.ss2d_matmul_fp8(_matmul(**{name: at + 4, "c": FAKE}), ws, 1 << 40, None)), name
+        assert lib.ss2d_matmul_fp8(_matmul(**{name: at + 2, "c": FAKE}), ws, 1 << 40, None) == MISALIGNED
+    assert accepted(_norm(lib, yd=2, sc=FAKE + 3 * GB + 4, y=FAKE))
+    assert _norm(lib, yd=2, sc=FAKE + 3 * GB + 2, y=FAKE) == MISALIGNED
+    assert accepted(lib.ss2d_linear_attention(_attention(lengths=FAKE + 9 * GB + 4, out=FAKE), ws, 1 << 40, None))
+    assert lib.ss2d_linear_attention(_attention(lengths=FAKE + 9 * GB + 1, out=FAKE), ws, 1 << 40, None) == MISALIGNED
+    assert accepted(lib.ss2d_linear_attention_step(_step(slots=FAKE + 4 * GB + 12, out=FAKE), None))
+    assert lib.ss2d_linear_attention_step(_step(slots=FAKE + 4 * GB + 2, out=FAKE), None) == MISALIGNED
