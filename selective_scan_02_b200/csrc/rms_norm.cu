@@ -323,12 +323,15 @@ cudaError_t rms_launch_types(const RmsArgs &a, cudaStream_t s)
                       : launch_early(rms_norm_kernel<TPR, NV, VEC, XBF16, kRnF32>, grid, kThreads, 0, s, 1, a);
 }
 
-template <int TPR, int NV>
+// SINGLE: widths that are not multiples of 8 come here too.
+template <int TPR, int NV, bool SINGLE = true>
 cudaError_t rms_launch(const RmsArgs &a, cudaStream_t s)
 {
     if (a.D % 8 == 0)
         return a.x_bf16 ? rms_launch_types<TPR, NV, true, true>(a, s) : rms_launch_types<TPR, NV, true, false>(a, s);
-    return a.x_bf16 ? rms_launch_types<TPR, NV, false, true>(a, s) : rms_launch_types<TPR, NV, false, false>(a, s);
+    if constexpr (SINGLE)
+        return a.x_bf16 ? rms_launch_types<TPR, NV, false, true>(a, s) : rms_launch_types<TPR, NV, false, false>(a, s);
+    return cudaErrorInvalidValue;
 }
 
 size_t rms_esize(int dtype) { return dtype == SS2D_F32 ? 4 : dtype == SS2D_BF16 ? 2 : 1; }
@@ -415,7 +418,7 @@ extern "C" int ss2d_rms_norm(const void *x, int x_dtype, const void *residual, i
     else if (!many && D <= 8192)
         e = rms_launch<1024, 1>(a, s);
     else if (D <= 16 * 24 && D % 8 == 0)  // (333 columns: 79 us so, 76 below)
-        e = rms_launch<16, 3>(a, s);
+        e = rms_launch<16, 3, false>(a, s);
     else if (D <= 32 * 16)
         e = rms_launch<32, 2>(a, s);
     else if (D <= 32 * 24)

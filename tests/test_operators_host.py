@@ -1,6 +1,8 @@
 """Host-side checks of the operators of a linear-attention layer: each entry point refuses what it does
 not take, with its status and before anything is enqueued.  The pointers are never dereferenced."""
 import ctypes
+import re
+import subprocess
 
 import pytest
 import torch
@@ -215,3 +217,14 @@ def test_what_is_read_number_by_number_may_lie_on_four_bytes(lib):
     assert lib.ss2d_linear_attention(_attention(lengths=FAKE + 9 * GB + 1, out=FAKE), ws, 1 << 40, None) == MISALIGNED
     assert accepted(lib.ss2d_linear_attention_step(_step(slots=FAKE + 4 * GB + 12, out=FAKE), None))
     assert lib.ss2d_linear_attention_step(_step(slots=FAKE + 4 * GB + 2, out=FAKE), None) == MISALIGNED
+
+
+def test_no_instance_of_the_norm_that_no_width_takes():
+    """The library's own symbols name an instance's threads a row, parts and whether its accesses are of eight columns;
+    sixteen threads of three parts are for multiples of 8 alone."""
+    names = subprocess.run(["nm", "-C", ss.LIB_PATH], capture_output=True, text=True).stdout
+    built = set(re.findall(r"rms_norm_kernel<(\d+), (\d+), (true|false)", names))
+    if not built:
+        pytest.skip("the library is stripped")
+    wide = {b[:2] for b in built if b[2] == "true"}
+    assert {b[:2] for b in built if b[2] == "false"} == wide - {("16", "3")} and ("16", "3") in wide
