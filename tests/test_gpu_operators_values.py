@@ -7,7 +7,7 @@ import torch
 import selective_scan_02_b200 as ss
 from tests import operator_reference as ref
 from tests.operator_reference import BF16, U
-from tests.test_gpu_operators import _attention_inputs, _check_norm, _gen, _within
+from tests.test_gpu_operators import _attention_inputs, _check_attention, _check_norm, _gen, _matmul_inputs, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -86,3 +86,53 @@ def test_a_nan_in_a_decay_reaches_no_token_before_its_own(shape):
     out, last = ss.linear_attention(q, k, v, bad, scale=scale, h0=h0, lengths=n, return_last_state=True)
     assert not out[:, :, 0].isfinite().any() and not last[:, 0].isfinite().any()
     assert out[:, :, 1:].isfinite().all() and last[:, 1:].isfinite().all()
+
+
+@pytest.mark.parametrize("batch,per_token", [(1, False), (1, True), (8, False), (8, True)])
+def test_states_of_hundreds_of_chunks_keep_their_bits(batch, per_token):
+    """300 chunks with slow decays, in one segment (a CTA for every head) and in several.
+
+    A chunk's sum enters the state with two roundings of at most a half-step of it.  As independent errors, evenly spread over a
+    step, 300 chunks that all count leave sqrt(600) U / sqrt(3) = 8.4e-7 of its norm, and the sums within a chunk little more:
+    1e-6.  One bf16 part of w V less is 1e-5, and a chunk's decay rounded to one fp32 number 2e-6 to 5e-6 where it is slow."""
+    L, D = 128 * 300, 64
+    rates = torch.tensor([m * 2.0 ** -e for e in (15, 17, 19) for m in (1.0, 1.21, 1.37, 1.53, 1.71, 1.9)], device="cuda")
+    H, g = len(rates), _gen(402)
+    k = torch.randn(batch, L, 1, D, device="cuda", generator=g).bfloat16()
+    v = torch.randn(batch, L, H, D, device="cuda", generator=g).bfloat16()
+    gates = -rates if not per_token else (-rates).expand(batch, L, H).contiguous()
+    ws = torch.empty(ss.linear_attention_workspace_size(batch, L, 1, H, D, D), dtype=torch.uint8, device="cuda")
+    assert (ws.numel() > 256) == (batch == 1)  # segments' states
+    _, last = ss.linear_attention(k, k, v, gates, return_last_state=True, workspace=ws)
+    ss.check_workspace_status(ws)
+    behind = torch.arange(L - 1, -1, -1, device="cuda", dtype=torch.float64)[:, None]
+    for b in range(batch):
+        for h in range(H):
+            weight = torch.exp(-rates[h].double() * behind)
+            want = k[b, :, 0].double().T @ (v[b, :, h].double() * weight)
+            err = ((last[b, h].double() - want).norm() / want.norm()).item()
+            assert err <= 1e-6, (b, h, err)
+
+
+@pytest.mark.parametrize("m,n,k", [(4, 1024, 2048), (24, 520, 4096), (100, 300, 1104), (333, 1000, 1104), (1000, 1024, 4096)])
+def test_products_keep_their_bits(m, n, k):
+    """fp32 outputs.  A block's 128 products are exact, and their sum is cut off below about 2^-25 of its largest term in each
+    of the MMAs' additions, or rounded; each block then takes one rounding: at most 64 blocks, sqrt(64) U / sqrt(3) = 2.8e-7 of
+    the norm as independent errors, and half as much again for the blocks' sums: 5e-7."""
+    a, sa, w, sw, bias = _matmul_inputs(m, n, k, m + n)
+    want, _ = ref.matmul_fp8(a, sa, w, sw, bias)
+    got = ss.matmul_fp8(a, sa, w, sw, bias=bias, out_dtype=torch.float32)
+    assert ((got.double() - want).norm() / want.norm()).item() <= 5e-7
+
+
+@pytest.mark.parametrize("shape", [(1, 390, 1, 2, 64, 64), (2, 700, 1, 2, 128, 96), (1, 6000, 1, 1, 64, 32)])
+def test_runs_of_resets(shape):
+    """Many tokens on end that reset the state, among slow decays: sums of thousands stand beside weights near one."""
+    B, L, G, H, Dk, Dv = shape
+    for value in (-math.inf, torch.finfo(torch.float32).min, -90.0):
+        q, k, v, gates, scale, h0 = _attention_inputs(shape, 403, True, True, True)
+        gates *= 0.05
+        for lo, hi in ((3, 30), (45, 64), (100, 228), (300, 331)):
+            gates[:, lo:hi] = value
+        out, last = ss.linear_attention(q, k, v, gates, scale=scale, h0=h0, return_last_state=True)
+        _check_attention(q, k, v, gates, scale, h0, None, out, last)
