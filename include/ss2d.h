@@ -424,6 +424,8 @@ int ss2d_diag_bounded_wait(int *error_word, long long spin_limit, void *stream);
  *            holds y / s rounded to e4m3 (nearest, ties to even): s times it stands for y.  A
  *            NaN becomes e4m3's NaN and does not enter the maximum.
  * residual_out : (rows, D) of the residual's type; may be `residual` itself (in place).
+ * The squares are summed in fp32 as well: a row's sum of r^2 must be below 2^128 (with more, y is 0), and with eps = 0
+ * its root mean square at least 2^-60.
  * D up to 32768 (16-byte accesses where D is a multiple of 8).  Deterministic. */
 int ss2d_rms_norm(const void *x, int x_dtype, const void *residual, int residual_dtype, const float *weight, float eps,
                   void *y, int y_dtype, float *scales, void *residual_out, long long rows, int D, void *stream);
@@ -494,7 +496,10 @@ size_t ss2d_linear_attention_workspace(const ss2d_linear_attention_args *args);
  * Log decays below -128 count as -128 (a decay of zero in fp32), so -infinity resets the state.
  * An infinity or a NaN in q, k or v, or a NaN in log_decay, makes what its token enters not finite (a NaN, or an
  * infinity), and reaches no earlier token and, of v, no other column.
- * The state and the sums are fp32; q, k, v and out are bf16.  Deterministic. */
+ * q, k, v and out are bf16, the state and the sums fp32.  Above 8 tokens the outputs are formed on the tensor cores from
+ * decayed scores and a copy of the state that are rounded to bf16 for it: each term of an output is off by up to 2^-8 of
+ * itself before the output's own rounding (in norm an output is off by about 2.3e-3, where one rounding is 1.7e-3).
+ * The state itself takes no such rounding.  Deterministic. */
 int ss2d_linear_attention(const ss2d_linear_attention_args *args, void *workspace, size_t workspace_bytes,
                           void *stream);
 

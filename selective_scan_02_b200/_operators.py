@@ -140,7 +140,8 @@ def rms_norm(x, weight, residual=None, eps=1e-6, out_dtype=torch.bfloat16, y=Non
     of y, then scales if y is float8_e4m3fn, then residual_out (r in the residual's type) if a
     residual is given.  out_dtype (float32, bfloat16 or float8_e4m3fn) is the type of a y
     allocated here; a given y keeps its own.  scales (..., ceil(D / 128)) fp32 holds one scale
-    for each 128 columns of a row.  residual_out may be `residual` itself.
+    for each 128 columns of a row.  residual_out may be `residual` itself.  A row's sum of r^2 must
+    be below 2^128.
     """
     call = (_marshal or _module()).rms_norm
     if stream is None:
@@ -187,7 +188,8 @@ def linear_attention(q, k, v, log_decay, scale=1.0, h0=None, lengths=None, retur
     `out` behind them are left as they were.  Returns out (B, L, H, Dv) bf16, or (out, h_last)
     with return_last_state or an h_last given (which may be h0 itself).  workspace: a tensor of
     at least linear_attention_workspace_size bytes, not shared by calls that overlap on the GPU;
-    allocated here when none is given.
+    allocated here when none is given.  States and sums are fp32; above 8 tokens, scores and the
+    state enter `out` rounded to bf16.
     """
     call = (_marshal or _module()).linear_attention
     if stream is None:

@@ -136,3 +136,16 @@ def test_runs_of_resets(shape):
             gates[:, lo:hi] = value
         out, last = ss.linear_attention(q, k, v, gates, scale=scale, h0=h0, return_last_state=True)
         _check_attention(q, k, v, gates, scale, h0, None, out, last)
+
+
+@pytest.mark.parametrize("rows,d", [(3, 256), (400, 301), (400, 8192)])
+def test_rms_norm_at_the_ends_of_its_range(rows, d):
+    """Sums of squares just below 2^128, and with an eps of 0 rows of a root mean square of 2^-60."""
+    x = torch.randn(rows, d, device="cuda", generator=_gen(d)).clamp_(-4, 4)
+    w = torch.randn(d, device="cuda", generator=_gen(d + 1))
+    x = x / x.square().mean(-1, keepdim=True).sqrt()
+    for size, eps in ((0.99 * 2.0 ** 64 / d ** 0.5, 1e-6), (2.0 ** -60, 0.0)):
+        for out in ("f32", "bf16", "e4m3"):
+            dt = {"f32": torch.float32, "bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}[out]
+            _check_norm(x * size, w, None, out, ss.rms_norm(x * size, w, eps=eps, out_dtype=dt),
+                        float(torch.tensor(eps, dtype=torch.float32)))
