@@ -85,7 +85,8 @@ struct ChunkedArgs {
     int *tickets;        // those taken; then, of each cut unit, the warps that have stored the first piece's state
 };
 
-template <int DK, int DV>
+// STATES: the first pass over segments, which has the state's products alone in tensor memory.
+template <int DK, int DV, bool STATES = false>
 struct Lc {
     static constexpr int kSlots = DK == 64 ? 3 : 2;      // of the rings of tiles: chunks in flight
     static constexpr int kDecays = DK == 64 ? 4 : 2;     // of the ring of decays
@@ -98,10 +99,10 @@ struct Lc {
     // Columns of tensor memory: scores (two buffers; P in place), P V, Q S, and K^T (w V), in as many buffers as
     // there is room for.  Of w V, all three parts in blocks of their own where they fit (one product), else the
     // first two, and the third is added to the second's (a product for each).
-    static constexpr uint32_t kScoresAt = 0, kOutAt = 256, kInterAt = kOutAt + DV, kDeltaAt = kInterAt + DV;
+    static constexpr uint32_t kScoresAt = 0, kOutAt = 256, kInterAt = kOutAt + DV, kDeltaAt = STATES ? 0 : kInterAt + DV;
     static constexpr int kBlocks = kDeltaAt + kLcParts * DV <= 512 ? kLcParts : kLcParts - 1;
-    static constexpr int kDelta = kBlocks * DV, kDeltas = (512 - (int)kDeltaAt) / kDelta;
-    static_assert(kDeltas >= 1, "tensor memory");
+    static constexpr int kDelta = kBlocks * DV, kDeltas = (int)kDeltaAt + 2 * kDelta <= 512 ? 2 : 1;
+    static_assert(kDeltaAt + kDeltas * kDelta <= 512, "tensor memory");
     // mbarriers: rings of kSlots, kDecays and kDeltas, then pairs, then single ones
     static constexpr int kQFull = 0, kKFull = kQFull + kSlots, kVFull = kKFull + kSlots, kQFree = kVFull + kSlots,
                          kKFree = kQFree + kSlots, kVFree = kKFree + kSlots, kDecFull = kVFree + kSlots,
@@ -181,8 +182,8 @@ template <int DK, int DV, int PASS>
 __device__ __forceinline__ void linear_chunked(const CUtensorMap &map_q, const CUtensorMap &map_k, const CUtensorMap &map_v,
                                                const ChunkedArgs &p, int index, int seg_from, int segs)
 {
-    using C = Lc<DK, DV>;
     constexpr bool STATES = PASS == kLcStates, CUT = PASS == kLcCut;
+    using C = Lc<DK, DV, STATES>;
     extern __shared__ __align__(1024) unsigned char smem[];
     const LinAttnArgs &a = p.a;
     const uint32_t base = tc::smem_u32(smem);
@@ -994,8 +995,10 @@ cudaError_t launch_width(const ChunkedArgs &p, cudaStream_t s)
     if (e == cudaSuccess)
         e = cut ? configure_smem(linear_chunked_kernel<DK, DV, kLcCut>, (int)Lc<DK, DV>::kSmem, configured[2])
                 : configure_smem(whole, (int)Lc<DK, DV>::kSmem, configured[sorted ? 3 : 0]);
+    constexpr size_t kAllSmem = Lc<DK, DV>::kSmem, kPassSmem = Lc<DK, DV, true>::kSmem;
+    constexpr size_t kFirstSmem = kAllSmem > kPassSmem ? kAllSmem : kPassSmem;
     if (e == cudaSuccess && p.nseg > 1)
-        e = configure_smem(linear_first_kernel<DK, DV>, (int)Lc<DK, DV>::kSmem, configured[1]);
+        e = configure_smem(linear_first_kernel<DK, DV>, (int)kFirstSmem, configured[1]);
     if (e != cudaSuccess)
         return e;
     if (cut) {
@@ -1006,7 +1009,7 @@ cudaError_t launch_width(const ChunkedArgs &p, cudaStream_t s)
     }
     if (p.nseg == 1)
         return launch_early(whole, units, kLcThreads, Lc<DK, DV>::kSmem, s, 1, q, k, v, part, 0, 1);
-    e = launch_early(linear_first_kernel<DK, DV>, units * (unsigned)(p.nseg - 1), kLcThreads, Lc<DK, DV>::kSmem, s, 1, q, k, v, part);
+    e = launch_early(linear_first_kernel<DK, DV>, units * (unsigned)(p.nseg - 1), kLcThreads, kFirstSmem, s, 1, q, k, v, part);
     const long long elements = (long long)a.B * a.H * a.Dk * a.Dv / 4;
     if (e == cudaSuccess)
         e = launch_early(linear_carry_kernel, (unsigned)((elements + kLcCarryThreads - 1) / kLcCarryThreads), kLcCarryThreads, 0, s,

@@ -32,7 +32,7 @@ static int g_ready, g_polls;
 template <int DK, int DV, bool STATES>
 void run(int warp, int chunks)
 {
-    using C = Lc<DK, DV>;
+    using C = Lc<DK, DV, STATES>;
     const uint32_t base = 0, tmem = 0;
     bool good = true;
     auto bar = [](int which) { return (uint32_t)which; };

@@ -13,7 +13,7 @@ struct Params { Args a; float *decays = g_decays; int nseg = 2; };
 template <bool STATES>
 void warp2(const Params &p, int t_first, int t_end)
 {
-    using C = Lc<128, 64>;
+    using C = Lc<128, 64, STATES>;
     static ChunkDecay decay[C::kDecays];
     const Args &a = p.a;
     const int lane = g_lane, h = 0, b = 0, seg = 0;

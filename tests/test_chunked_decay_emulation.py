@@ -56,7 +56,7 @@ def emulator(tmp_path_factory):
     head = open(os.path.join(csrc, "linear_attention.h")).read()
     clamp = head[head.index("constexpr int kLaMaxDim"):head.index("// One call over whole sequences")]
     constants = src[src.index("constexpr int kLcChunk"):src.index("struct ChunkedArgs")]
-    shapes = src[src.index("template <int DK, int DV>\nstruct Lc"):src.index("// kind::f16, fp32 accumulate")]
+    shapes = src[src.index("template <int DK, int DV, bool STATES = false>\nstruct Lc"):src.index("// kind::f16, fp32 accumulate")]
     first = "} else if (warp == 2) {"
     at = src.index(first) + len(first)
     warp = src[at:src.index("} else if (warp >= kLcWeight", at)]

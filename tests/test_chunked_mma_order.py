@@ -30,7 +30,7 @@ def _between(src, first, last):
 def emulator(tmp_path_factory):
     src = open(SOURCE).read()
     constants = src[src.index("constexpr int kLcChunk"):src.index("struct ChunkedArgs")]
-    shapes = src[src.index("template <int DK, int DV>\nstruct Lc"):src.index("__device__ __forceinline__ uint32_t lc_pack")]
+    shapes = src[src.index("template <int DK, int DV, bool STATES = false>\nstruct Lc"):src.index("__device__ __forceinline__ uint32_t lc_pack")]
     scores = _between(src, "} else if (warp == 1 && !STATES) {", "} else if (warp == 3) {")
     state = _between(src, "} else if (warp == 3) {", "} else if (warp == 2) {")
     header = ("#pragma once\nnamespace ss2d {\n" + constants + shapes + "}\n")
