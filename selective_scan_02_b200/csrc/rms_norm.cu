@@ -9,9 +9,11 @@
 // A row stays in registers between the reduction of its squares and the output, so each
 // tensor is read or written once: the kernel is bounded by device memory, and what matters is to keep
 // enough loads in flight and the instructions few.  16384 rows of 4096 columns (bf16 with a bf16 residual,
-// e4m3 out): 74 us, 6.4 TB/s, the rate of a plain copy; 100352 rows of 96 (fp32 in, bf16 out): 20 us, 6.7
-// TB/s.  Eight rows are 2.6 us on the GPU, most of it the launch.  CTAs that stay and walk the rows, with or
-// without an asynchronous ring of loads, took longer: other rows' CTAs hide one row's reduction better.
+// e4m3 out): 79.5 us a call on rows that change, 5.9 TB/s, 71 in a graph on the same ones (a part of them stays in L2);
+// 100352 rows of 96 (fp32 in, bf16 out): 21.4 and 19.4 us, 6.3 TB/s.  Eight rows are 2.9 us on the GPU, most of it the
+// launch.  Rows of single columns, whose accesses are of an element each, take up to 1.9 times as long (333 columns 70
+// us, 37 at 384).  CTAs that stay and walk the rows, with or without an asynchronous ring of loads, took longer: other
+// rows' CTAs hide one row's reduction better.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <stddef.h>
@@ -323,15 +325,12 @@ cudaError_t rms_launch_types(const RmsArgs &a, cudaStream_t s)
                       : launch_early(rms_norm_kernel<TPR, NV, VEC, XBF16, kRnF32>, grid, kThreads, 0, s, 1, a);
 }
 
-// SINGLE: widths that are not multiples of 8 come here too.
-template <int TPR, int NV, bool SINGLE = true>
+template <int TPR, int NV>
 cudaError_t rms_launch(const RmsArgs &a, cudaStream_t s)
 {
     if (a.D % 8 == 0)
         return a.x_bf16 ? rms_launch_types<TPR, NV, true, true>(a, s) : rms_launch_types<TPR, NV, true, false>(a, s);
-    if constexpr (SINGLE)
-        return a.x_bf16 ? rms_launch_types<TPR, NV, false, true>(a, s) : rms_launch_types<TPR, NV, false, false>(a, s);
-    return cudaErrorInvalidValue;
+    return a.x_bf16 ? rms_launch_types<TPR, NV, false, true>(a, s) : rms_launch_types<TPR, NV, false, false>(a, s);
 }
 
 size_t rms_esize(int dtype) { return dtype == SS2D_F32 ? 4 : dtype == SS2D_BF16 ? 2 : 1; }
@@ -395,10 +394,11 @@ extern "C" int ss2d_rms_norm(const void *x, int x_dtype, const void *residual, i
     a.eps = eps;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     // Many rows: 16 or 24 columns a thread, whichever fits the row better, so that each has several loads in flight, a
-    // row needs few warps and few threads have no column.  (2^25 elements, bf16 with a bf16 residual to e4m3: 5120 columns
-    // 43 us in 256 threads of 24, 55 in 512 of 16;  24576 columns 45 us in 1024 of 24, 73 in 1024 of 32.)  Few rows (less
-    // than two for each SM): 8 columns a thread, the shortest way through a row.  Narrow rows: as many lanes as they need
-    // (100352 rows of 7, 33, 100 columns: 33 us with a warp for each row, 4, 10, 18 so).
+    // row needs few warps and few threads have no column.  (2^25 elements, bf16 with a bf16 residual to e4m3: 333 columns
+    // 70 us in 16 threads of 24, 85 in 32 of 16;  5120 columns 41 us in 256 of 24, 59 in 512 of 16;  24576 columns 50 us in
+    // 1024 of 24, 51 in 1024 of 32.)  Few rows (less than two for each of the B200's 148 SMs): 8 columns a thread, the
+    // shortest way through a row.  Narrow rows: as many lanes as they need (100352 rows of 7, 33, 100 columns: 38 to 40 us
+    // with a warp for each row, 4.5, 9.7, 18 so).
     const bool many = rows > 2 * 148;
     cudaError_t e;
     if (D <= 8)
@@ -417,8 +417,8 @@ extern "C" int ss2d_rms_norm(const void *x, int x_dtype, const void *residual, i
         e = rms_launch<256, 1>(a, s);
     else if (!many && D <= 8192)
         e = rms_launch<1024, 1>(a, s);
-    else if (D <= 16 * 24 && D % 8 == 0)  // (333 columns: 79 us so, 76 below)
-        e = rms_launch<16, 3, false>(a, s);
+    else if (D <= 16 * 24)
+        e = rms_launch<16, 3>(a, s);
     else if (D <= 32 * 16)
         e = rms_launch<32, 2>(a, s);
     else if (D <= 32 * 24)

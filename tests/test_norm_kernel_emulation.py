@@ -68,7 +68,7 @@ def emulator(tmp_path_factory):
     at = src.index("    if (D <= 8)\n")
     dispatch = src[at:src.index(";", src.index("    else\n", at)) + 1]
     launch = """
-template <int TPR, int NV, bool SINGLE = true>
+template <int TPR, int NV>
 int rms_launch(const RmsArgs &a, int)
 {
     constexpr int kThreads = TPR > kRnThreads ? TPR : kRnThreads;
@@ -82,8 +82,7 @@ int rms_launch(const RmsArgs &a, int)
         return a.res_bf16 ? run(rms_norm_kernel<TPR, NV, V, false, kRnBf16>) : 1;
     };
     if (a.D % 8 == 0) return types(std::true_type{});
-    if constexpr (SINGLE) return types(std::false_type{});
-    return 1;
+    return types(std::false_type{});
 }
 """
     header = '#pragma once\n#include "common_emu.h"\n' + EXTRA + "namespace ss2d {\n" + body + launch + "}\n"

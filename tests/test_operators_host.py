@@ -1,6 +1,7 @@
 """Host-side checks of the operators of a linear-attention layer: each entry point refuses what it does
 not take, with its status and before anything is enqueued.  The pointers are never dereferenced."""
 import ctypes
+import os
 import re
 import subprocess
 
@@ -219,12 +220,13 @@ def test_what_is_read_number_by_number_may_lie_on_four_bytes(lib):
     assert lib.ss2d_linear_attention_step(_step(slots=FAKE + 4 * GB + 2, out=FAKE), None) == MISALIGNED
 
 
-def test_no_instance_of_the_norm_that_no_width_takes():
-    """The library's own symbols name an instance's threads a row, parts and whether its accesses are of eight columns;
-    sixteen threads of three parts are for multiples of 8 alone."""
+def test_no_instance_of_the_norm_that_no_width_takes(lib):
+    """The library's own symbols name an instance's threads a row and parts; the entry point's rule names those that it takes,
+    for widths that are multiples of 8 and others."""
     names = subprocess.run(["nm", "-C", ss.LIB_PATH], capture_output=True, text=True).stdout
     built = set(re.findall(r"rms_norm_kernel<(\d+), (\d+), (true|false)", names))
     if not built:
         pytest.skip("the library is stripped")
-    wide = {b[:2] for b in built if b[2] == "true"}
-    assert {b[:2] for b in built if b[2] == "false"} == wide - {("16", "3")} and ("16", "3") in wide
+    source = open(os.path.join(os.path.dirname(ss.LIB_PATH), "csrc", "rms_norm.cu")).read()
+    rule = set(re.findall(r"e = rms_launch<(\d+), (\d+)>\(a, s\)", source))
+    assert {b[:2] for b in built if b[2] == "false"} == {b[:2] for b in built if b[2] == "true"} == rule
