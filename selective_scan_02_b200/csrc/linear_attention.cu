@@ -49,8 +49,8 @@ int la_check_stride(const char *call, const char *name, long long size, long lon
 }
 
 // Sequences that run token by token: with few tokens a chunk of 128 is mostly padding.  (Token by token and in
-// chunks, 16 heads of 128 x 128: one sequence of 4, 8, 16 tokens 5.1, 8.5, 15.4 and 8.0 us throughout; 64
-// sequences of 8 and 16 tokens 58, 109 and 106 us.)
+// chunks, 16 heads of 128 x 128: one sequence of 4, 8, 16 tokens 5.4, 8.9, 15.7 and 8.9 us throughout; 64
+// sequences of 8 and 16 tokens 57 and 103, in chunks 118 both.)
 constexpr int kLaRecurrentTokens = 8;
 
 size_t la_workspace(const ss2d_linear_attention_args &a)

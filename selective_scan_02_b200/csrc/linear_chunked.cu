@@ -33,12 +33,12 @@
 // what lies between, and the pass above starts each segment from the state before it.  The first segment needs no first
 // pass: it goes beside the others' ones, in the same launch.
 //
-// What bounds it: a chunk of 128 x 64 columns takes about 3700 cycles.  Shared memory passes 2950 cycles' worth of bytes
-// in them (tiles in, w V out, and the MMAs' operands: 64 columns read all of Q and K), the warps issue 0.6 instructions a
-// cycle and scheduler, the tensor cores are busy 40 %, and hand-overs between the warps (load, scores, P, P V, output;
-// K^T w V, state, Q S) fill the rest.  32768 tokens of 16 heads of 128 x 128: 214 us, of which the first pass
-// is 68 (floor 82 us, bytes); 32 x 3136 tokens of 6 heads of 64 x 32: 58 us (floor 16).  Without its arithmetic, barriers
-// and MMAs alone, the kernel takes three quarters of its time.
+// What bounds it: a chunk of 128 x 64 columns takes about 4000 cycles.  Shared memory passes 3200 cycles' worth of bytes
+// in them (tiles in, w V out, and the MMAs' operands: 64 columns read all of Q and K, and a product for each part of w V
+// reads K three times), the warps issue 0.55 instructions a cycle and scheduler, the tensor cores are busy 42 %, and
+// hand-overs between the warps (load, scores, P, P V, output; K^T w V, state, Q S) fill the rest.  32768 tokens of 16
+// heads of 128 x 128: 217 to 280 us by what the power limit leaves of the clock, of which the first pass is a third
+// (floor 82 us, bytes); 32 x 3136 tokens of 6 heads of 64 x 32: 61 to 67 us (floor 16).
 #include "api_internal.h"
 #include "launch_util.h"
 #include "linear_attention.h"
@@ -56,7 +56,7 @@ constexpr int kLcParts = 3;           // of w V
 constexpr int kLcAhead = 3;           // chunks that a tile is asked for in L2 before its load
 constexpr int kLcIdlePolls = 1 << 24;  // of the copy warp and of a second piece, at 120 ns or more: about 2 s
 constexpr int kLcStateWarps = 8;
-constexpr int kLcSms = 148;
+constexpr int kLcSms = 148;  // of a B200; the plan, and the workspace with it, follow from the sizes alone, without a device
 constexpr int kLcMaxSegments = 149;  // one CTA for each SM in either pass
 
 constexpr float kLcLog2e = 1.4426950408889634f, kLcLn2 = 0.6931471805599453f;
@@ -988,7 +988,7 @@ cudaError_t launch_width(const ChunkedArgs &p, cudaStream_t s)
     part.units = (int)((long long)a.B * a.H * ((a.Dv + DV - 1) / DV));
     const unsigned units = (unsigned)part.units;
     // The longest sequences first, so that the last CTAs to end have little to do, where there is more than one CTA for
-    // an SM and a warp can sort them.  (Seven of up to 1531 tokens, 32 heads of 128 x 64: 48.6 us as they come, 46.0 so.)
+    // an SM and a warp can sort them.  (Seven of up to 1531 tokens, 32 heads of 128 x 64: 45.3 us as they come, 38.6 so.)
     const bool sorted = a.lengths && a.B > 1 && a.B <= 32 && p.nseg == 1 && units > (unsigned)kLcSms;
     const auto whole = sorted ? linear_chunked_kernel<DK, DV, kLcSorted> : linear_chunked_kernel<DK, DV, kLcAll>;
     const bool cut = p.cut && !sorted;
@@ -1026,12 +1026,13 @@ int lc_cols(const LinAttnArgs &a) { return a.Dv <= 32 ? 32 : 64; }
 // Segments of a sequence, and cut units, by the time that they take in tenths of a chunk's: whole waves of CTAs, two
 // or three chunks to fill and drain a CTA, 0.55 of a chunk's time for one of the first pass (the first segment, which
 // needs no such pass, is shorter than the others so as to end with theirs), and what the launches and the sums between
-// the passes take.  (us for 16 heads of 128 x 128: 2048 tokens, 1, 3, 4 segments: 38, 39, 35;  32768 tokens, 4, 5,
-// 9, 10: 247, 212, 230, 244.  One head of 128 x 64, 65536 tokens, 24, 48, 75, 103: 83, 53, 44, 41.)
+// the passes take.  (us for 16 heads of 128 x 128: 2048 tokens, 1, 3, 4, 5 segments: 40, 39, 36, 40;  32768 tokens, 4,
+// 5, 9, 10: 286, 227, 232, 226.  One head of 128 x 64, 65536 tokens, 24, 103: 82, 40.)
 //
 // Where the units fill the last of several waves by half or less, those of that wave are cut in two instead: the first
 // pieces go first, the second ones behind the whole units, when what they start from is long there (they wait for it all
-// the same), and both together fill the SMs.  (Up to 32 sequences with lengths are sorted instead, which evens out more.)
+// the same), and both together fill the SMs: 32 x 3136 tokens of 6 heads of 64 x 32, 75 us uncut, 62 so.  (Up to 32
+// sequences with lengths are sorted instead, which evens out more.)
 void lc_plan(const LinAttnArgs &a, ChunkedArgs *p)
 {
     const long long units = (long long)a.B * a.H * ((a.Dv + lc_cols(a) - 1) / lc_cols(a));

@@ -18,12 +18,12 @@
 //                 the CTAs of a cluster, which add up in distributed shared memory: the weights' bytes
 //                 bound a product with few tokens, and this spreads their reading over all SMs.
 //
-// 8192 x 6144 x 4096: 195 to 229 us by what the power limit leaves of the clock, 1.8 to 2.1 PFLOP/s.  A block
+// 8192 x 6144 x 4096: 190 to 233 us by what the power limit leaves of the clock, 1.8 to 2.1 PFLOP/s.  A block
 // of K of a 128 x 256 tile takes 866 cycles; its 48 KB pass through shared memory twice (written by TMA, read by
 // the MMAs), 768 cycles at 128 bytes a cycle, and that bounds the kernel; the tensor cores are busy 53 %.  A pair of
 // CTAs on one 256 x 256 tile reads less, but has room for two buffers of partial products only, and waiting
-// across the pair for them took 414 us.  4 tokens x 6144 x 2048: 4.5 us (13 MB of weights, 1.9 us at the copy's
-// rate); 333 x 1000 x 1104: 7.7 us, the latency of a launch, nine blocks and the cluster's sum.
+// across the pair for them took 414 us.  4 tokens x 6144 x 2048: 4.9 us (13 MB of weights, 1.9 us at the copy's
+// rate); 333 x 1000 x 1104: 10.3 us in a graph, the latency of a launch and nine blocks in 24 CTAs.
 #include <cuda_bf16.h>
 #include <stddef.h>
 #include <stdint.h>
