@@ -80,3 +80,51 @@ def test_launches_that_wait_for_room():
         torch.cuda.synchronize()
     assert end - start > 0.1, "no launch waited"
     assert ticks.widest(start, end) < (end - start) / 2
+
+
+def test_calls_from_several_threads():
+    """Threads that call at once, each on a stream of its own; the first of them makes the first calls of its kinds."""
+    g = torch.Generator("cuda").manual_seed(5)
+
+    def normal(*s):
+        return torch.randn(*s, device="cuda", generator=g)
+
+    def attention(B, L, H, D):
+        q, v, gates = normal(B, L, 1, D).bfloat16(), normal(B, L, H, D).bfloat16(), torch.full((H,), -0.03, device="cuda")
+        return lambda: ss.linear_attention(q, q, v, gates, return_last_state=True)
+
+    def product(m, n, k):
+        a, w = (normal(x, k).clamp(-4, 4).to(torch.float8_e4m3fn) for x in (m, n))
+        sa, sw = normal(m, -(-k // 128)).abs(), normal(-(-n // 128), -(-k // 128)).abs()
+        return lambda: (ss.matmul_fp8(a, sa, w, sw),)
+
+    def norm(rows, d):
+        x, w = normal(rows, d), normal(d)
+        return lambda: ss.rms_norm(x, w, out_dtype=torch.float8_e4m3fn)
+
+    calls = [attention(20, 700, 8, 64), attention(1, 6000, 2, 96), attention(3, 6, 2, 40), product(5, 300, 1104),
+             product(90, 300, 2048), norm(40, 1000)]
+    got = [[] for _ in calls]
+    failed = []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(20):
+                    got[i].append(calls[i]())
+                s.synchronize()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    for call, results in zip(calls, got):
+        want = call()
+        assert len(results) == 20 and all(torch.equal(x.float(), y.float()) for r in results for x, y in zip(r, want))
+    ss.check_workspace_status()
