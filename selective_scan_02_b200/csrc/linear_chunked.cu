@@ -74,7 +74,7 @@ struct alignas(16) ChunkDecay {
 struct ChunkedArgs {
     LinAttnArgs a;
     // For every segment but the last: (B * H, nseg - 1, Dk, Dv) its own state, then that of the sequence behind it, and
-    // (B * H, nseg - 1) its decay
+    // (B * H, nseg - 1) its decay, or, with the sign set, a slow one less 1
     float *states, *decays;
     int nseg, first_chunks, seg_chunks;  // chunks of the first segment, and of the others
     int units;                           // of one segment: a CTA's columns of one head of one sequence
@@ -553,7 +553,8 @@ __device__ __forceinline__ void linear_chunked(const CUtensorMap &map_q, const C
             arrive(C::kDecFull + dec.slot);
         }
         if (STATES && lane == 0 && good)
-            p.decays[bh * (p.nseg - 1) + seg] = exp2f((float)whole);
+            p.decays[bh * (p.nseg - 1) + seg] =
+                whole > -0.5 ? copysignf(expm1f((float)(whole * (double)kLcLn2)), -1.0f) : exp2f((float)whole);
     } else if (warp >= kLcWeight && warp < (STATES ? kLcState : kLcScore)) {
         // V -> w V, 16 bytes at a time.  A part is the upper 16 bits of what the
         // parts before it leave, so the subtractions are exact and three parts hold all 24 bits.
@@ -931,7 +932,8 @@ __global__ void __launch_bounds__(kLcTicketThreads) linear_tickets_kernel(int *t
 }
 
 // The segments' own states -> the state behind each: one thread for four elements of a head's state, with the
-// loads of kLcCarry segments on their way at once.
+// loads of kLcCarry segments on their way at once.  A slow decay comes less 1, for over a hundred segments would add up
+// what its rounding to fp32 loses (4e-6 of the state, 3e-7 so).
 constexpr int kLcCarry = 8, kLcCarryThreads = 128;
 
 __global__ void __launch_bounds__(kLcCarryThreads) linear_carry_kernel(float *states, const float *decays, int segs, int size4,
@@ -956,8 +958,9 @@ __global__ void __launch_bounds__(kLcCarryThreads) linear_carry_kernel(float *st
 #pragma unroll
         for (int i = 0; i < kLcCarry; ++i)
             if (i0 + i < segs) {
-                s = make_float4(fmaf(s.x, by[i], own[i].x), fmaf(s.y, by[i], own[i].y), fmaf(s.z, by[i], own[i].z),
-                                fmaf(s.w, by[i], own[i].w));
+                const float keep = __float_as_uint(by[i]) >> 31 ? 1.0f : 0.0f;
+                s = make_float4(fmaf(s.x, keep, fmaf(s.x, by[i], own[i].x)), fmaf(s.y, keep, fmaf(s.y, by[i], own[i].y)),
+                                fmaf(s.z, keep, fmaf(s.z, by[i], own[i].z)), fmaf(s.w, keep, fmaf(s.w, by[i], own[i].w)));
                 at[(long long)(i0 + i) * size4] = s;
             }
     }

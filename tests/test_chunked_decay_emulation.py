@@ -170,9 +170,14 @@ def test_a_nan_reaches_no_token_before_its_own(emulator, tmp_path, at):
         _check(got[0], part)
 
 
-def test_a_segment_s_decay(emulator, tmp_path):
+@pytest.mark.parametrize("rate", [0.0, 1e-7, 2e-5, 3e-4, 0.002, 0.3])
+def test_a_segment_s_decay(emulator, tmp_path, rate):
+    """Of a slow one, the decay less 1, whose roundings are of its own size."""
     rng = np.random.default_rng(9)
-    gates = (-0.002 * rng.exponential(size=1000)).astype(np.float32)
+    gates = (-rate * rng.exponential(size=1000)).astype(np.float32)
     _, decay = _run(emulator, tmp_path, gates, 128, 900, states=True)
-    want = np.exp(gates[128:900].astype(np.float64).sum())
-    assert abs(decay - want) <= 64 * U * want
+    total = gates[128:900].astype(np.float64).sum()
+    if np.signbit(np.float32(decay)):
+        assert total >= -0.36 and abs(decay - np.expm1(total)) <= 64 * U * abs(total) + 1e-45
+    else:
+        assert total <= -0.34 and abs(decay - np.exp(total)) <= 64 * U * max(1, -total) * np.exp(total) + 2.0 ** -126  # (fp32's least)

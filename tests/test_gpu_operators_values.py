@@ -149,3 +149,20 @@ def test_rms_norm_at_the_ends_of_its_range(rows, d):
             dt = {"f32": torch.float32, "bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}[out]
             _check_norm(x * size, w, None, out, ss.rms_norm(x * size, w, eps=eps, out_dtype=dt),
                         float(torch.tensor(eps, dtype=torch.float32)))
+
+
+@pytest.mark.parametrize("heads,chunks", [(1, 600), (2, 600), (1, 2048)])
+def test_states_of_many_segments_keep_their_bits(heads, chunks):
+    """Over a hundred segments: bounds as for the chunks of one, the segments' sums being a tenth as many."""
+    L, D = 128 * chunks, 64
+    g = _gen(404)
+    k = torch.randn(1, L, 1, D, device="cuda", generator=g).bfloat16()
+    v = torch.randn(1, L, heads, D, device="cuda", generator=g).bfloat16()
+    assert ss.linear_attention_workspace_size(1, L, 1, heads, D, D) > 60 * heads * D * D * 4
+    behind = torch.arange(L - 1, -1, -1, device="cuda", dtype=torch.float64)[:, None]
+    for rate in [m * 2.0 ** -e for e in (15, 17, 19, 21) for m in (1.0, 1.21, 1.53, 1.9)]:
+        gates = torch.full((heads,), -rate, device="cuda")
+        _, last = ss.linear_attention(k, k, v, gates, return_last_state=True)
+        want = k[0, :, 0].double().T @ (v[0, :, -1].double() * torch.exp(gates[0].double() * behind))
+        err = ((last[0, -1].double() - want).norm() / want.norm()).item()
+        assert err <= 1e-6, (rate, err)

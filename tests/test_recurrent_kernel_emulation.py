@@ -167,3 +167,21 @@ def test_carry(emulator, tmp_path, heads, segments, Dk, Dv):
         size[:, i] += size[:, i - 1] * decays[:, i, None, None]
     err = np.abs(got.numpy().reshape(states.shape) - want)
     assert (err <= size * segments * U).all()
+
+
+def test_carry_of_slow_decays(emulator, tmp_path):
+    """Decays near 1 come less 1: the state behind 140 segments keeps its bits (each takes two roundings of a half-step; as
+    independent errors sqrt(280) U / sqrt(3) of the norm, 5.8e-7), where rounded decays would lose 140 half-steps of their own."""
+    rng = np.random.default_rng(4)
+    heads, segments, D = 2, 140, 16
+    states = rng.standard_normal((heads, segments, D, D)).astype(np.float32)
+    less = -(2.0 ** -rng.uniform(9, 24, (heads, 1)) * np.ones((1, segments)))
+    less[1, ::7] = 0.0  # no decay at all
+    less = np.copysign(less, -1.0).astype(np.float32)
+    got = _run(emulator, tmp_path, 4, heads, segments, 1, heads, D, D, False, 0, state=states, gates=less)
+    want = states.astype(np.float64)
+    for i in range(1, segments):
+        want[:, i] += want[:, i - 1] * (1.0 + less[:, i, None, None].astype(np.float64))
+    last, exact = got.numpy().reshape(states.shape)[:, -1], want[:, -1]
+    err = np.linalg.norm(last - exact, axis=(1, 2)) / np.linalg.norm(exact, axis=(1, 2))
+    assert (err <= 6e-7).all(), err
