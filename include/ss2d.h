@@ -521,7 +521,8 @@ typedef struct ss2d_linear_attention_step_args {
     const int *slots;       /* (B) int32 in device memory: the state of row b; a row whose slot is not within
                                0 .. pool - 1 is empty, and its row of out is left as it was.  Rows of one
                                slot are consecutive tokens of one sequence, in the order of the rows.
-                               NULL: row b has state b (pool >= B). */
+                               NULL: row b has state b (pool >= B).  Rows are compared with one another, so B is
+                               at most 65536 with slots (and 8192 rows already take longer by it). */
     float scale;
     float *state;           /* (pool, H, Dk, Dv) fp32, updated in place */
     void *out;              /* (B, H, Dv) bf16 */

@@ -212,7 +212,8 @@ def linear_attention_step(q, k, v, log_decay, state, slots=None, scale=1.0, out=
     q, k (B, G, Dk) and v (B, H, Dv) bf16 (strided as for linear_attention); log_decay (H) or
     (B, H) fp32; state (pool, H, Dk, Dv) fp32.  slots (B) int32 names the state of each row
     (None: row b has state b); a row whose slot is outside the pool is empty and its row of `out`
-    is left as it was, and rows of one slot are consecutive tokens in the order of the rows.
+    is left as it was, and rows of one slot are consecutive tokens in the order of the rows (at
+    most 65536 rows with slots).
     """
     call = (_marshal or _module()).linear_attention_step
     if stream is None:

@@ -230,3 +230,10 @@ def test_no_instance_of_the_norm_that_no_width_takes(lib):
     source = open(os.path.join(os.path.dirname(ss.LIB_PATH), "csrc", "rms_norm.cu")).read()
     rule = set(re.findall(r"e = rms_launch<(\d+), (\d+)>\(a, s\)", source))
     assert {b[:2] for b in built if b[2] == "false"} == {b[:2] for b in built if b[2] == "true"} == rule
+
+
+def test_a_step_of_too_many_rows_with_slots_is_refused(lib):
+    wide = dict(B=65537, pool=65537, H=2, G=2, Dk=8, Dv=8)
+    assert lib.ss2d_linear_attention_step(_step(**wide), None) == UNSUPPORTED and b"slots" in lib.ss2d_last_error()
+    # without slots it is not (the refusal is the overlap's)
+    assert lib.ss2d_linear_attention_step(_step(**wide, slots=None, out=FAKE), None) == INVALID
